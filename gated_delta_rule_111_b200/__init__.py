@@ -18,12 +18,19 @@ Functions (same names as the C ABI):
   gdn2_chunk_fwd_logits(xq, xk, xv, xa, xb, xw, S0=None, ...) -> (o, S_T)  prefill from BF16 logits
   gdn2_recurrent_step(q, k, v, alpha, b, w, S, ...)   -> o          in-place decode step
   gdn2_output_gate(o, g, weight, eps, ...)            -> y          RMS norm + sigmoid output gate
+  gdn2_output_gate_bwd(dy, o, g, weight, eps, ...)    -> dict       its gradient
+  gdn2_residual_norm(x, r, weight, eps, ...)          -> (h, y, rstd)  residual add (scale, dropout) + RMS norm
+  gdn2_residual_norm_bwd(dy, h, rstd, weight, ...)    -> dict       its gradient
+  gdn2_slot_steps(q, k, v, alpha, b, w, pool, slots, ...) -> o      tokens against a cache of states
+  gdn2_slot_steps_logits(xq, xk, xv, xa, xb, xw, pool, slots, ...) -> o  the same from BF16 logits
+  gdn2_state_copy(pool, src, dst, ...)                -> pool       copy, fork, compact, free cached states
   gdn2_chunk_bwd(q, k, v, alpha, b, w, S0, dO, dST, ...) -> dict    gradients of every input
   gdn2_chunk_bwd_workspace_size(B, T, H, dk, dv)      -> bytes      workspace of gdn2_chunk_bwd
   gdn2_chunk_bwd_noalloc(..., out)                    -> dict       the same, workspace inside the library
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -33,7 +40,10 @@ import torch
 from . import build as _build
 
 __all__ = ["gdn2_chunk_fwd", "gdn2_chunk_fwd_from_host", "gdn2_chunk_fwd_varlen", "gdn2_chunk_fwd_segmented", "gdn2_chunk_fwd_segmented_workspace_size",
-           "gdn2_chunk_fwd_segments", "gdn2_chunk_fwd_logits", "gdn2_output_gate", "gdn2_recurrent_step", "gdn2_chunk_bwd",
+           "gdn2_chunk_fwd_segments", "gdn2_chunk_fwd_logits", "gdn2_output_gate", "gdn2_output_gate_bwd",
+           "gdn2_output_gate_bwd_workspace_size", "gdn2_residual_norm", "gdn2_residual_norm_bwd",
+           "gdn2_residual_norm_bwd_workspace_size", "gdn2_slot_steps", "gdn2_slot_steps_logits", "gdn2_state_copy",
+           "gdn2_recurrent_step", "gdn2_chunk_bwd",
            "gdn2_chunk_bwd_workspace_size", "gdn2_chunk_bwd_noalloc", "gdn2_device_error", "gdn2_set_wait_limit", "library_path",
            "load_library", "exported_symbols",
            "GDN2_OK", "GDN2_ERR_INVALID_ARG", "GDN2_ERR_UNSUPPORTED", "GDN2_ERR_CUDA", "Gdn2Error"]
@@ -79,6 +89,22 @@ def load_library(rebuild_if_stale: bool = True) -> ctypes.CDLL:
     lib.gdn2_chunk_fwd_logits.restype = i
     lib.gdn2_output_gate.argtypes = [vp, vp, fp, ctypes.c_float, vp, i, i, i, i, i, vp]
     lib.gdn2_output_gate.restype = i
+    f, d = ctypes.c_float, ctypes.c_double
+    lib.gdn2_output_gate_bwd.argtypes = [vp, vp, vp, fp, f, vp, vp, fp, vp, sz, i, i, i, i, i, vp]
+    lib.gdn2_output_gate_bwd.restype = i
+    lib.gdn2_output_gate_bwd_workspace_size.argtypes = [i]
+    lib.gdn2_output_gate_bwd_workspace_size.restype = sz
+    lib.gdn2_residual_norm.argtypes = [vp, vp, fp, fp, d, vp, f, vp, vp, fp, i, i, i, i, vp]
+    lib.gdn2_residual_norm.restype = i
+    lib.gdn2_residual_norm_bwd.argtypes = [vp, vp, fp, fp, vp, vp, fp, d, vp, vp, vp, fp, fp, vp, sz, i, i, i, i, vp]
+    lib.gdn2_residual_norm_bwd.restype = i
+    lib.gdn2_residual_norm_bwd_workspace_size.argtypes = [i, i]
+    lib.gdn2_residual_norm_bwd_workspace_size.restype = sz
+    for fn in (lib.gdn2_slot_steps, lib.gdn2_slot_steps_logits):
+        fn.argtypes = [vp] * 12 + [f, vp] + [i] * (7 if fn is lib.gdn2_slot_steps else 6) + [vp]
+        fn.restype = i
+    lib.gdn2_state_copy.argtypes = [fp, fp, vp, vp, i, i, i, i, i, i, i, vp]
+    lib.gdn2_state_copy.restype = i
     lib.gdn2_recurrent_step.argtypes = [vp, vp, vp, fp, fp, fp, fp, vp, i, i, i, i, i, vp]
     lib.gdn2_recurrent_step.restype = i
     lib.gdn2_chunk_bwd.argtypes = [vp, vp, vp, fp, fp, fp, fp, vp, fp, vp, vp, vp, fp, fp, fp, fp, vp, sz,
@@ -125,6 +151,14 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+_current = contextlib.nullcontext()
+
+
+def _on(device):
+    """A context in which ``device`` is current; the one that is current already costs nothing to enter."""
+    return _current if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _need(t, name, dtype, shape, device):
@@ -403,6 +437,272 @@ def gdn2_output_gate(o, g, weight, eps=1e-6, *, y=None, stream=None):
         _check(lib.gdn2_output_gate(_ptr(o), _ptr(g), _ptr(weight), float(eps), _ptr(y), B, T, H, dv, code,
                                     _stream(stream, dev)))
     return y
+
+
+def _rows(shape) -> int:
+    """B * T of a [B, T, D] tensor, as the C ABI's int."""
+    if len(shape) != 3:
+        raise ValueError(f"expected a [B, T, D] tensor, got shape {tuple(shape)}")
+    rows = shape[0] * shape[1]
+    if rows > 0x7fffffff:
+        raise ValueError("B * T must be below 2^31")
+    return rows
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor from the pool of the stream the call runs on, so that the memory of a workspace freed
+    after the call is reused behind the call's kernels and not beside them."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(workspace, need, device, stream):
+    if workspace is None:
+        return _empty((max(need, 16),), torch.uint8, device, stream)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor on the inputs' device")
+    return workspace
+
+
+def _dropout(p, rng, device):
+    """The call's p as a float, and rng checked where it is read."""
+    p = float(p)
+    if p > 0.0:
+        if rng is None:
+            raise ValueError("dropout (p > 0) needs rng, an int64 tensor of (seed, offset)")
+        _need(rng, "rng", torch.int64, (2,), device)
+        return p, rng
+    return p, None
+
+
+def gdn2_residual_norm(x, r, weight, eps=1e-6, *, scale=None, p=0.0, rng=None, h=None, y=None, rstd=None,
+                       stream=None):
+    """The norm in front of a block with the residual addition before it:
+    h = x + scale * dropout(r), y = h / sqrt(mean(h^2) + eps) * weight.  x [B,T,D] (bf16 or fp32: the
+    residual stream), r [B,T,D] (the branch: bf16, or fp32 beside an fp32 stream) or None; weight and
+    scale [D] fp32 (scale None: 1).  Dropout with probability ``p`` draws its mask from ``rng``, an int64
+    CUDA tensor (seed, offset).  Returns (h, y, rstd): h in x's dtype (x itself where r is None), y in
+    r's (x's where r is None, unless ``y`` is given), rstd [B,T] fp32.  h may be x and y may be r (in place)."""
+    lib = load_library()
+    if x.device.type != "cuda":
+        raise ValueError("gdn2_residual_norm needs CUDA tensors (there is no CPU implementation)")
+    shape, dev, sdt = x.shape, x.device, x.dtype
+    rows, D = _rows(shape), shape[2]
+    dt = r.dtype if r is not None else y.dtype if y is not None else sdt
+    scode, code = _dtype_code(x), _dtype_code(r if r is not None else y if y is not None else x)
+    _need(x, "x", sdt, shape, dev)
+    _need(weight, "weight", torch.float32, (D,), dev)
+    if r is not None:
+        _need(r, "r", dt, shape, dev)
+    if scale is not None:
+        _need(scale, "scale", torch.float32, (D,), dev)
+    p, rng = _dropout(p, rng, dev)
+    if r is None:
+        if h is not None:
+            raise ValueError("h: there is no addition to write without r")
+    elif h is None:
+        h = _empty(shape, sdt, dev, stream)
+    else:
+        _need(h, "h", sdt, shape, dev)
+    if y is None:
+        y = _empty(shape, dt, dev, stream)
+    else:
+        _need(y, "y", dt, shape, dev)
+    if rstd is None:
+        rstd = _empty(shape[:2], torch.float32, dev, stream)
+    else:
+        _need(rstd, "rstd", torch.float32, shape[:2], dev)
+    with _on(dev):
+        _check(lib.gdn2_residual_norm(_ptr(x), _ptr(r), _ptr(weight), _ptr(scale), p, _ptr(rng), float(eps), _ptr(h),
+                                      _ptr(y), _ptr(rstd), rows, D, scode, code, _stream(stream, dev)))
+    return (x if r is None else h), y, rstd
+
+
+def gdn2_residual_norm_bwd_workspace_size(rows: int, D: int) -> int:
+    """Bytes of device workspace gdn2_residual_norm_bwd needs for B * T = rows."""
+    return int(load_library().gdn2_residual_norm_bwd_workspace_size(rows, D))
+
+
+def gdn2_residual_norm_bwd(dy, h, rstd, weight, *, dh=None, r=None, scale=None, p=0.0, rng=None, branch=True,
+                           workspace=None, out=None, stream=None):
+    """Gradients through gdn2_residual_norm from its outputs h and rstd: dy [B,T,D] in y's dtype, dh [B,T,D]
+    in h's dtype (the gradient of h from its later uses) or None.  ``scale``, ``p`` and ``rng`` as in the
+    forward call (the same mask is drawn again); r (needed with scale) as there.  Returns a dict with dx (h's
+    dtype), dr (dy's dtype; None with ``branch`` False), dweight and dscale ([D] fp32; dscale None without
+    scale).  ``out``: a dict of preallocated gradients (dx may be dh); ``workspace``: a uint8 CUDA tensor
+    of at least gdn2_residual_norm_bwd_workspace_size bytes."""
+    lib = load_library()
+    if dy.device.type != "cuda":
+        raise ValueError("gdn2_residual_norm_bwd needs CUDA tensors (there is no CPU implementation)")
+    shape, dev, dt, sdt = dy.shape, dy.device, dy.dtype, h.dtype
+    rows, D = _rows(shape), shape[2]
+    scode, code = _dtype_code(h), _dtype_code(dy)
+    _need(dy, "dy", dt, shape, dev)
+    _need(h, "h", sdt, shape, dev)
+    _need(rstd, "rstd", torch.float32, shape[:2], dev)
+    _need(weight, "weight", torch.float32, (D,), dev)
+    if dh is not None:
+        _need(dh, "dh", sdt, shape, dev)
+    if not branch and (scale is not None or float(p) > 0.0):
+        raise ValueError("scale and dropout belong to a branch")
+    if scale is not None:
+        _need(scale, "scale", torch.float32, (D,), dev)
+        if r is None:
+            raise ValueError("the gradient of scale needs r")
+        _need(r, "r", dt, shape, dev)
+    p, rng = _dropout(p, rng, dev)
+    out = out or {}
+    g = {}
+    for name, want, s, d in (("dx", True, shape, sdt), ("dr", branch, shape, dt),
+                             ("dweight", True, (D,), torch.float32), ("dscale", scale is not None, (D,), torch.float32)):
+        t = out.get(name) if want else None
+        if t is not None:
+            _need(t, name, d, s, dev)
+        elif want:
+            t = _empty(s, d, dev, stream)
+        g[name] = t
+    with _on(dev):
+        ws = _workspace(workspace, int(lib.gdn2_residual_norm_bwd_workspace_size(rows, D)), dev, stream)
+        _check(lib.gdn2_residual_norm_bwd(_ptr(dy), _ptr(h), _ptr(rstd), _ptr(weight), _ptr(dh),
+                                          _ptr(r) if scale is not None else None, _ptr(scale), p, _ptr(rng),
+                                          _ptr(g["dx"]), _ptr(g["dr"]), _ptr(g["dweight"]), _ptr(g["dscale"]),
+                                          _ptr(ws), ws.numel() * ws.element_size(), rows, D, scode, code,
+                                          _stream(stream, dev)))
+    return g
+
+
+def gdn2_output_gate_bwd_workspace_size(dv: int) -> int:
+    """Bytes of device workspace gdn2_output_gate_bwd needs."""
+    return int(load_library().gdn2_output_gate_bwd_workspace_size(dv))
+
+
+def gdn2_output_gate_bwd(dy, o, g, weight, eps=1e-6, *, workspace=None, out=None, stream=None):
+    """Gradients through gdn2_output_gate: dy, o, g [B,T,H,dv] (bf16 or fp32, same dtype), weight [dv] fp32.
+    Returns a dict with do, dg (dy's dtype) and dweight [dv] fp32.  ``out``: a dict of preallocated
+    gradients; ``workspace``: a uint8 CUDA tensor of at least gdn2_output_gate_bwd_workspace_size bytes."""
+    lib = load_library()
+    if dy.device.type != "cuda":
+        raise ValueError("gdn2_output_gate_bwd needs CUDA tensors (there is no CPU implementation)")
+    B, T, H, dv = shape = dy.shape
+    dev, dt = dy.device, dy.dtype
+    code = _dtype_code(dy)
+    _need(dy, "dy", dt, shape, dev)
+    _need(o, "o", dt, shape, dev)
+    _need(g, "g", dt, shape, dev)
+    _need(weight, "weight", torch.float32, (dv,), dev)
+    out = out or {}
+    grads = {}
+    for name, s, d in (("do", shape, dt), ("dg", shape, dt), ("dweight", (dv,), torch.float32)):
+        t = out.get(name)
+        if t is None:
+            t = _empty(s, d, dev, stream)
+        else:
+            _need(t, name, d, s, dev)
+        grads[name] = t
+    with _on(dev):
+        ws = _workspace(workspace, int(lib.gdn2_output_gate_bwd_workspace_size(dv)), dev, stream)
+        _check(lib.gdn2_output_gate_bwd(_ptr(dy), _ptr(o), _ptr(g), _ptr(weight), float(eps), _ptr(grads["do"]),
+                                        _ptr(grads["dg"]), _ptr(grads["dweight"]), _ptr(ws),
+                                        ws.numel() * ws.element_size(), B, T, H, dv, code, _stream(stream, dev)))
+    return grads
+
+
+def _slot_steps(name, gates, q, k, v, alpha, b, w, pool, slots, cu_seqlens, keep, g, weight, eps, o, stream):
+    """Checks and the call of gdn2_slot_steps (gates fp32) and gdn2_slot_steps_logits (everything bf16)."""
+    lib = load_library()
+    if q.device.type != "cuda":
+        raise ValueError(f"{name} needs CUDA tensors (there is no CPU implementation)")
+    T, H, dk = q.shape
+    dv = v.shape[-1]
+    dev, dt = q.device, q.dtype if gates is torch.float32 else torch.bfloat16
+    code = _dtype_code(q)
+    _need(q, "q", dt, (T, H, dk), dev)
+    _need(k, "k", dt, (T, H, dk), dev)
+    _need(v, "v", dt, (T, H, dv), dev)
+    _need(alpha, "alpha", gates, (T, H, dk), dev)
+    _need(b, "b", gates, (T, H, dk), dev)
+    _need(w, "w", gates, (T, H, dv), dev)
+    if slots.dim() != 1:
+        raise ValueError("slots: expected a 1-D tensor, one slot per sequence")
+    N, n_slots = slots.shape[0], pool.shape[0]
+    _need(pool, "pool", torch.float32, (n_slots, H, dk, dv), dev)
+    _need(slots, "slots", torch.int32, (N,), dev)
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
+    elif T != N:
+        raise ValueError(f"{N} sequences with {T} tokens: without cu_seqlens every sequence has one token")
+    if keep is not None:
+        _need(keep, "keep", torch.int32, (N,), dev)
+    if (g is None) != (weight is None):
+        raise ValueError("the epilogue needs both g and weight")
+    if g is not None:
+        _need(g, "g", dt, (T, H, dv), dev)
+        _need(weight, "weight", torch.float32, (dv,), dev)
+    if o is None:
+        o = _empty((T, H, dv), dt, dev, stream)
+    else:
+        _need(o, "o", dt, (T, H, dv), dev)
+    args = (_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(b), _ptr(w), _ptr(pool), _ptr(slots), _ptr(cu_seqlens),
+            _ptr(keep), _ptr(g), _ptr(weight), float(eps), _ptr(o), N, T, H, n_slots, dk, dv)
+    with _on(dev):
+        if gates is torch.float32:
+            _check(lib.gdn2_slot_steps(*args, code, _stream(stream, dev)))
+        else:
+            _check(lib.gdn2_slot_steps_logits(*args, _stream(stream, dev)))
+    return o
+
+
+def gdn2_slot_steps(q, k, v, alpha, b, w, pool, slots, cu_seqlens=None, *, keep=None, g=None, weight=None, eps=1e-6,
+                    o=None, stream=None):
+    """Tokens of N sequences against a cache of states, the states updated in place.  q,k [T,H,dk], v [T,H,dv]
+    (bf16 or fp32); alpha,b [T,H,dk], w [T,H,dv] fp32; pool [n_slots,H,dk,dv] fp32; slots int32 [N] (a slot
+    outside the pool, such as -1, marks padding: its outputs are zero); cu_seqlens int32 [N+1] (None: one token
+    per sequence, T = N); keep int32 [N]: how many of a sequence's tokens its stored state takes in (None:
+    all).  With g [T,H,dv] and weight [dv], o goes through the output epilogue.  Returns o [T,H,dv]; rows
+    behind the last sequence are not written."""
+    return _slot_steps("gdn2_slot_steps", torch.float32, q, k, v, alpha, b, w, pool, slots, cu_seqlens, keep, g, weight,
+                       eps, o, stream)
+
+
+def gdn2_slot_steps_logits(xq, xk, xv, xa, xb, xw, pool, slots, cu_seqlens=None, *, keep=None, g=None, weight=None,
+                           eps=1e-6, o=None, stream=None):
+    """gdn2_slot_steps from BF16 pre-activation logits (the input preparation of gdn2_chunk_fwd_logits inside
+    the kernel); the other arguments as there, g bf16.  Returns o [T,H,dv] bf16."""
+    return _slot_steps("gdn2_slot_steps_logits", torch.bfloat16, xq, xk, xv, xa, xb, xw, pool, slots, cu_seqlens, keep, g,
+                       weight, eps, o, stream)
+
+
+def gdn2_state_copy(pool, src, dst, *, source=None, stream=None):
+    """Copies states between slots: pool[dst[i]] becomes what pool[src[i]] (``source``[src[i]] when another
+    pool is given) was before the call; src -1 zeroes the destination.  pool [n_slots,H,dk,dv] or, all layers
+    at once, [layers,n_slots,H,dk,dv] fp32; src, dst int32 [n], n at most 4096.  Pairs with an index out of
+    range are skipped; of several pairs with one destination the last counts.  Returns pool."""
+    lib = load_library()
+    if pool.device.type != "cuda":
+        raise ValueError("gdn2_state_copy needs CUDA tensors (there is no CPU implementation)")
+    if pool.dim() not in (4, 5):
+        raise ValueError(f"pool: expected [n_slots,H,dk,dv] or [layers,n_slots,H,dk,dv], got {tuple(pool.shape)}")
+    dev = pool.device
+    n_dst, H, dk, dv = pool.shape[-4:]
+    layers = pool.shape[0] if pool.dim() == 5 else 1
+    _need(pool, "pool", torch.float32, pool.shape, dev)
+    n_src = n_dst
+    if source is not None:
+        if source.dim() != pool.dim():
+            raise ValueError("source: expected as many dimensions as pool has")
+        n_src = source.shape[-4]
+        _need(source, "source", torch.float32, (*pool.shape[:-4], n_src, H, dk, dv), dev)
+    if src.dim() != 1:
+        raise ValueError("src: expected a 1-D tensor")
+    n = src.shape[0]
+    _need(src, "src", torch.int32, (n,), dev)
+    _need(dst, "dst", torch.int32, (n,), dev)
+    with _on(dev):
+        _check(lib.gdn2_state_copy(_ptr(pool if source is None else source), _ptr(pool), _ptr(src), _ptr(dst), n, layers,
+                                   n_src, n_dst, H, dk, dv, _stream(stream, dev)))
+    return pool
 
 
 def gdn2_recurrent_step(q, k, v, alpha, b, w, S, *, o=None, stream=None):

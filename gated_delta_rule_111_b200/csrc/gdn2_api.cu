@@ -8,6 +8,7 @@
 namespace gdn2 {
 void set_wait_limit(long long cycles);
 cudaError_t read_device_error(unsigned int *value, bool clear);
+cudaError_t read_slot_conflict(unsigned int *value, bool clear);
 }  // namespace gdn2
 
 namespace {
@@ -48,6 +49,62 @@ bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
     return pa < pb + nb && pb < pa + na;
 }
 
+// A buffer argument: `n` bytes, `align` the alignment it needs, `twin` the index of
+// the input that an output may be itself (exactly), or -1.
+struct Buf {
+    const void *p;
+    size_t n;
+    const char *name;
+    bool optional = false;
+    unsigned align = 16;
+    int twin = -1;
+};
+
+gdn2_status check_buf(const Buf &b) {
+    if (!b.p) return b.optional || b.n == 0 ? GDN2_OK : fail(GDN2_ERR_INVALID_ARG, "null pointer: %s", b.name);
+    if (reinterpret_cast<uintptr_t>(b.p) & (b.align - 1)) {
+        snprintf(g_last_error, sizeof(g_last_error), "pointer not %u-byte aligned: %s", b.align, b.name);
+        return GDN2_ERR_INVALID_ARG;
+    }
+    return GDN2_OK;
+}
+
+// Every buffer present and aligned; no output overlaps an input (but for its twin) or another output.
+template <int NI, int NO> gdn2_status check_bufs(const Buf (&ins)[NI], const Buf (&outs)[NO]) {
+    gdn2_status st;
+    for (const Buf &b : ins)
+        if ((st = check_buf(b)) != GDN2_OK) return st;
+    for (const Buf &b : outs)
+        if ((st = check_buf(b)) != GDN2_OK) return st;
+    for (int o = 0; o < NO; ++o) {
+        for (int i = 0; i < NI; ++i) {
+            if (i == outs[o].twin && ins[i].p == outs[o].p) continue;
+            if (overlaps(outs[o].p, outs[o].n, ins[i].p, ins[i].n)) {
+                snprintf(g_last_error, sizeof(g_last_error), "%s overlaps %s", outs[o].name, ins[i].name);
+                return GDN2_ERR_INVALID_ARG;
+            }
+        }
+        for (int i = o + 1; i < NO; ++i)
+            if (overlaps(outs[o].p, outs[o].n, outs[i].p, outs[i].n)) {
+                snprintf(g_last_error, sizeof(g_last_error), "%s overlaps %s", outs[o].name, outs[i].name);
+                return GDN2_ERR_INVALID_ARG;
+            }
+    }
+    return GDN2_OK;
+}
+
+gdn2_status check_norm(int rows, int D, double p, const void *rng, gdn2_dtype stream_dt, gdn2_dtype dt) {
+    if (rows < 0) return fail(GDN2_ERR_INVALID_ARG, "%s", "negative rows");
+    if ((stream_dt != GDN2_BF16 && stream_dt != GDN2_FP32) || (dt != GDN2_BF16 && dt != GDN2_FP32))
+        return fail(GDN2_ERR_UNSUPPORTED, "%s", "unknown dtype");
+    if (stream_dt == GDN2_BF16 && dt == GDN2_FP32)
+        return fail(GDN2_ERR_UNSUPPORTED, "%s", "a BF16 residual stream with an FP32 branch");
+    if (D < 1 || D > 16384) return fail(GDN2_ERR_UNSUPPORTED, "%s", "D must be 1 to 16384");
+    if (!(p >= 0.0 && p < 1.0)) return fail(GDN2_ERR_INVALID_ARG, "%s", "p must be in [0, 1)");
+    if (p > 0.0 && !rng) return fail(GDN2_ERR_INVALID_ARG, "%s", "dropout needs rng");
+    return GDN2_OK;
+}
+
 }  // namespace
 
 namespace gdn2 {
@@ -70,7 +127,7 @@ const char *gdn2_status_string(gdn2_status s) {
 
 const char *gdn2_last_error(void) { return g_last_error; }
 
-int gdn2_version(void) { return 200; }
+int gdn2_version(void) { return 300; }
 
 gdn2_status gdn2_set_wait_limit(long long cycles) {
     gdn2::set_wait_limit(cycles > 0 ? cycles : 4000000000ll);
@@ -79,7 +136,11 @@ gdn2_status gdn2_set_wait_limit(long long cycles) {
 
 gdn2_status gdn2_device_error(unsigned int *code, int clear) {
     if (!code) return fail(GDN2_ERR_INVALID_ARG, "%s", "null pointer: code");
-    return cuda_status(gdn2::read_device_error(code, clear != 0), "gdn2_device_error");
+    unsigned int conflict = 0;
+    cudaError_t err = gdn2::read_device_error(code, clear != 0);
+    if (err == cudaSuccess) err = gdn2::read_slot_conflict(&conflict, clear != 0);
+    if (err == cudaSuccess && conflict) *code |= 0x10000u;
+    return cuda_status(err, "gdn2_device_error");
 }
 
 // Shared host-side checks and dispatch of the two prefill entry points.  nseq
@@ -422,6 +483,179 @@ gdn2_status gdn2_recurrent_step(const void *q, const void *k, const void *v, con
     cudaError_t err = gdn2::launch_recurrent_step(q, k, v, alpha, b, w, S, o, B, H, d_k, d_v, dt,
                                                   static_cast<cudaStream_t>(stream));
     return cuda_status(err, "gdn2_recurrent_step launch");
+}
+
+gdn2_status gdn2_residual_norm(const void *x, const void *r, const float *weight, const float *scale, double p,
+                               const uint64_t *rng, float eps, void *h, void *y, float *rstd, int rows, int D,
+                               gdn2_dtype stream_dt, gdn2_dtype dt, void *stream) {
+    g_last_error[0] = 0;
+    gdn2_status st = check_norm(rows, D, p, rng, stream_dt, dt);
+    if (st != GDN2_OK) return st;
+    if (!(eps >= 0.f) || eps > 3.0e38f) return fail(GDN2_ERR_INVALID_ARG, "%s", "eps must be finite and >= 0");
+    if (!r && (scale || p > 0.0 || h))
+        return fail(GDN2_ERR_INVALID_ARG, "%s", "scale, dropout and h need the branch r");
+    if (rows == 0) return GDN2_OK;
+    const size_t n = (size_t)rows * D, sb = n * (stream_dt == GDN2_BF16 ? 2 : 4), bb = n * (dt == GDN2_BF16 ? 2 : 4);
+    const Buf ins[] = {{x, sb, "x"},
+                       {r, bb, "r", true},
+                       {weight, (size_t)D * 4, "weight"},
+                       {scale, (size_t)D * 4, "scale", true},
+                       {p > 0.0 ? rng : nullptr, 16, "rng", true, 8}};
+    const Buf outs[] = {{h, sb, "h", r == nullptr, 16, 0}, {y, bb, "y", false, 16, 1}, {rstd, (size_t)rows * 4, "rstd"}};
+    if ((st = check_bufs(ins, outs)) != GDN2_OK) return st;
+    return cuda_status(gdn2::launch_residual_norm(x, r, weight, scale, p, reinterpret_cast<const unsigned long long *>(rng),
+                                                  eps, h, y, rstd, rows, D, stream_dt, dt,
+                                                  static_cast<cudaStream_t>(stream)),
+                       "gdn2_residual_norm launch");
+}
+
+size_t gdn2_residual_norm_bwd_workspace_size(int rows, int D) {
+    if (rows <= 0 || D < 1 || D > 16384) return 0;
+    return gdn2::residual_norm_bwd_workspace_bytes(rows, D);
+}
+
+gdn2_status gdn2_residual_norm_bwd(const void *dy, const void *h, const float *rstd, const float *weight,
+                                   const void *dh, const void *r, const float *scale, double p, const uint64_t *rng,
+                                   void *dx, void *dr, float *dweight, float *dscale, void *workspace,
+                                   size_t workspace_bytes, int rows, int D, gdn2_dtype stream_dt, gdn2_dtype dt,
+                                   void *stream) {
+    g_last_error[0] = 0;
+    gdn2_status st = check_norm(rows, D, p, rng, stream_dt, dt);
+    if (st != GDN2_OK) return st;
+    if (dscale && (!scale || (!r && rows)))
+        return fail(GDN2_ERR_INVALID_ARG, "%s", "dscale needs r and scale");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t n = (size_t)rows * D, sb = n * (stream_dt == GDN2_BF16 ? 2 : 4), bb = n * (dt == GDN2_BF16 ? 2 : 4);
+    const size_t need = gdn2_residual_norm_bwd_workspace_size(rows, D);
+    const Buf ins[] = {{dy, bb, "dy"},
+                       {h, sb, "h"},
+                       {rstd, (size_t)rows * 4, "rstd"},
+                       {weight, rows ? (size_t)D * 4 : 0, "weight"},
+                       {dh, sb, "dh", true},
+                       {dscale ? r : nullptr, bb, "r", true},
+                       {scale, (size_t)D * 4, "scale", true},
+                       {p > 0.0 ? rng : nullptr, 16, "rng", true, 8}};
+    const Buf outs[] = {{dx, sb, "dx", false, 16, 4},
+                        {dr, bb, "dr", true, 16},
+                        {dweight, (size_t)D * 4, "dweight"},
+                        {dscale, (size_t)D * 4, "dscale", true},
+                        {workspace, need, "workspace"}};
+    if ((st = check_bufs(ins, outs)) != GDN2_OK) return st;
+    if (rows == 0) {                       // sums over no rows
+        cudaError_t err = cudaMemsetAsync(dweight, 0, (size_t)D * 4, s);
+        if (err == cudaSuccess && dscale) err = cudaMemsetAsync(dscale, 0, (size_t)D * 4, s);
+        return cuda_status(err, "gdn2_residual_norm_bwd of no rows");
+    }
+    if (workspace_bytes < need)
+        return fail(GDN2_ERR_INVALID_ARG, "%s", "workspace smaller than gdn2_residual_norm_bwd_workspace_size");
+    return cuda_status(gdn2::launch_residual_norm_bwd(dy, h, rstd, weight, dh, r, scale, p,
+                                                      reinterpret_cast<const unsigned long long *>(rng), dx, dr, dweight,
+                                                      dscale, static_cast<float *>(workspace), rows, D, stream_dt, dt, s),
+                       "gdn2_residual_norm_bwd launch");
+}
+
+size_t gdn2_output_gate_bwd_workspace_size(int d_v) {
+    return d_v == 64 || d_v == 128 ? gdn2::output_gate_bwd_workspace_bytes(d_v) : 0;
+}
+
+gdn2_status gdn2_output_gate_bwd(const void *dy, const void *o, const void *g, const float *weight, float eps,
+                                 void *d_o, void *d_g, float *dweight, void *workspace, size_t workspace_bytes, int B,
+                                 int T, int H, int d_v, gdn2_dtype dt, void *stream) {
+    g_last_error[0] = 0;
+    if (B < 0 || T < 0 || H < 0) return fail(GDN2_ERR_INVALID_ARG, "%s", "negative size");
+    if (dt != GDN2_BF16 && dt != GDN2_FP32) return fail(GDN2_ERR_UNSUPPORTED, "%s", "unknown dtype");
+    if (d_v != 64 && d_v != 128) return fail(GDN2_ERR_UNSUPPORTED, "%s", "d_v must be 64 or 128");
+    if (!(eps >= 0.f) || eps > 3.0e38f) return fail(GDN2_ERR_INVALID_ARG, "%s", "eps must be finite and >= 0");
+    const long long rows = (long long)B * T * H;
+    const size_t n = (size_t)rows * d_v * (dt == GDN2_BF16 ? 2 : 4), wn = (size_t)d_v * 4;
+    const size_t need = rows ? gdn2_output_gate_bwd_workspace_size(d_v) : 0;
+    const Buf ins[] = {{dy, n, "dy"}, {o, n, "o"}, {g, n, "g"}, {weight, rows ? wn : 0, "weight"}};
+    const Buf outs[] = {{d_o, n, "do"}, {d_g, n, "dg"}, {dweight, wn, "dweight"}, {workspace, need, "workspace"}};
+    gdn2_status st = check_bufs(ins, outs);
+    if (st != GDN2_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (rows == 0) return cuda_status(cudaMemsetAsync(dweight, 0, wn, s), "gdn2_output_gate_bwd of no rows");
+    if (workspace_bytes < need)
+        return fail(GDN2_ERR_INVALID_ARG, "%s", "workspace smaller than gdn2_output_gate_bwd_workspace_size");
+    return cuda_status(gdn2::launch_output_gate_bwd(dy, o, g, weight, eps, d_o, d_g, dweight,
+                                                    static_cast<float *>(workspace), rows, d_v, dt, s),
+                       "gdn2_output_gate_bwd launch");
+}
+
+// Shared checks and dispatch of the two slot steps.
+static gdn2_status slot_steps_common(const void *q, const void *k, const void *v, const void *alpha, const void *b,
+                                     const void *w, bool logits, float *pool, const int32_t *slots,
+                                     const int32_t *cu_seqlens, const int32_t *keep, const void *gate,
+                                     const float *weight, float eps, void *o, int N, int T_total, int H, int n_slots,
+                                     int d_k, int d_v, gdn2_dtype dt, void *stream) {
+    g_last_error[0] = 0;
+    gdn2_status st = check_common(N, H, d_k, d_v, dt);
+    if (st != GDN2_OK) return st;
+    if (T_total < 0 || n_slots < 0) return fail(GDN2_ERR_INVALID_ARG, "%s", "negative T_total or n_slots");
+    if (!cu_seqlens && T_total != N)
+        return fail(GDN2_ERR_INVALID_ARG, "%s", "without cu_seqlens every sequence has one token: T_total must be N");
+    if ((gate != nullptr) != (weight != nullptr))
+        return fail(GDN2_ERR_INVALID_ARG, "%s", "the epilogue needs both g and weight");
+    if (gate && (!(eps >= 0.f) || eps > 3.0e38f))
+        return fail(GDN2_ERR_INVALID_ARG, "%s", "eps must be finite and >= 0");
+    if (N == 0 || H == 0 || T_total == 0) return GDN2_OK;
+    if ((long long)N * H > 0x7fffffffll) return fail(GDN2_ERR_UNSUPPORTED, "%s", "N * H must be below 2^31");
+    const size_t es = dt == GDN2_BF16 ? 2 : 4, gs = logits ? 2 : 4, tok = (size_t)T_total * H;
+    const Buf ins[] = {{q, tok * d_k * es, "q"},
+                       {k, tok * d_k * es, "k"},
+                       {v, tok * d_v * es, "v"},
+                       {alpha, tok * d_k * gs, "alpha"},
+                       {b, tok * d_k * gs, "b"},
+                       {w, tok * d_v * gs, "w"},
+                       {slots, (size_t)N * 4, "slots", false, 4},
+                       {cu_seqlens, ((size_t)N + 1) * 4, "cu_seqlens", true, 4},
+                       {keep, (size_t)N * 4, "keep", true, 4},
+                       {gate, tok * d_v * es, "g", true},
+                       {weight, (size_t)d_v * 4, "weight", true}};
+    const Buf outs[] = {{pool, (size_t)n_slots * H * d_k * d_v * 4, "pool"}, {o, tok * d_v * es, "o"}};
+    if ((st = check_bufs(ins, outs)) != GDN2_OK) return st;
+    return cuda_status(gdn2::launch_slot_steps(q, k, v, alpha, b, w, logits, pool, slots, cu_seqlens, keep, gate, weight,
+                                               eps, o, N, T_total, H, n_slots, d_k, d_v, dt,
+                                               static_cast<cudaStream_t>(stream)),
+                       "gdn2_slot_steps launch");
+}
+
+gdn2_status gdn2_slot_steps(const void *q, const void *k, const void *v, const float *alpha, const float *b,
+                            const float *w, float *pool, const int32_t *slots, const int32_t *cu_seqlens,
+                            const int32_t *keep, const void *g, const float *weight, float eps, void *o, int N,
+                            int T_total, int H, int n_slots, int d_k, int d_v, gdn2_dtype dt, void *stream) {
+    return slot_steps_common(q, k, v, alpha, b, w, false, pool, slots, cu_seqlens, keep, g, weight, eps, o, N, T_total,
+                             H, n_slots, d_k, d_v, dt, stream);
+}
+
+gdn2_status gdn2_slot_steps_logits(const void *xq, const void *xk, const void *xv, const void *xa, const void *xb,
+                                   const void *xw, float *pool, const int32_t *slots, const int32_t *cu_seqlens,
+                                   const int32_t *keep, const void *g, const float *weight, float eps, void *o, int N,
+                                   int T_total, int H, int n_slots, int d_k, int d_v, void *stream) {
+    return slot_steps_common(xq, xk, xv, xa, xb, xw, true, pool, slots, cu_seqlens, keep, g, weight, eps, o, N, T_total,
+                             H, n_slots, d_k, d_v, GDN2_BF16, stream);
+}
+
+gdn2_status gdn2_state_copy(const float *src_pool, float *dst_pool, const int32_t *src, const int32_t *dst, int n,
+                            int layers, int n_src, int n_dst, int H, int d_k, int d_v, void *stream) {
+    g_last_error[0] = 0;
+    gdn2_status st = check_common(layers, H, d_k, d_v, GDN2_FP32);
+    if (st != GDN2_OK) return st;
+    if (n < 0 || n_src < 0 || n_dst < 0) return fail(GDN2_ERR_INVALID_ARG, "%s", "negative n, n_src or n_dst");
+    if (n == 0 || layers == 0 || H == 0 || n_dst == 0) return GDN2_OK;
+    if (n > gdn2::state_copy_max_pairs()) return fail(GDN2_ERR_UNSUPPORTED, "%s", "more than 4096 pairs in one call");
+    const size_t state = (size_t)H * d_k * d_v;
+    if (state / 4 > 0x7fffffffull) return fail(GDN2_ERR_UNSUPPORTED, "%s", "a state of 2^35 bytes or more");
+    if (src_pool == dst_pool && n_src != n_dst)
+        return fail(GDN2_ERR_INVALID_ARG, "%s", "one pool as source and destination needs n_src = n_dst");
+    const Buf ins[] = {{src_pool, (size_t)layers * n_src * state * 4, "src_pool"},
+                       {src, (size_t)n * 4, "src", false, 4},
+                       {dst, (size_t)n * 4, "dst", false, 4}};
+    const Buf outs[] = {{dst_pool, (size_t)layers * n_dst * state * 4, "dst_pool", false, 16, 0}};
+    if ((st = check_bufs(ins, outs)) != GDN2_OK) return st;
+    return cuda_status(gdn2::launch_state_copy(src_pool, dst_pool, src, dst, n, layers, n_src, n_dst, state,
+                                               static_cast<cudaStream_t>(stream)),
+                       "gdn2_state_copy launch");
 }
 
 }  // extern "C"

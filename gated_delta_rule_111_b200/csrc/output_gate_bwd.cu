@@ -1,0 +1,171 @@
+// Gradient of the output epilogue y = o / sqrt(mean(o^2) + eps) * weight * sigmoid(g)
+// (output_gate.cu), per (token, head) row of d_v channels.  With
+// rstd = 1 / sqrt(mean(o^2) + eps), n = o rstd, s = sigmoid(g), t = dy weight s:
+//   do = rstd (t - n mean(t n)),   dg = dy n weight s (1 - s),   dweight = sum_rows dy n s.
+//
+// Memory-bound: o, g and dy are read once, do and dg written once.  A lane holds 16
+// bytes of a row (8 BF16 or 4 FP32 channels), so a row takes 8 to 32 lanes and its
+// two sums are shuffles among them; rstd is formed again from o rather than kept by
+// the forward.  A warp issues the loads of kUnroll row groups before it reduces any.
+// dweight adds up in registers over the rows of a lane, then over the CTA in shared
+// memory; each CTA writes one row of partial sums, and a second launch adds those in
+// a fixed order, so the result does not change from call to call.
+#include "common.cuh"
+
+namespace gdn2 {
+namespace {
+
+using bf16 = __nv_bfloat16;
+constexpr int kThreads = 256;
+constexpr int kUnroll = 2;
+constexpr int kMaxGrid = 148 * 4;
+
+template <typename T> struct Lane;
+template <> struct Lane<bf16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void unpack(uint4 r, float (&v)[8]) {
+        const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(u[e] << 16);
+            v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+            u[e] = *reinterpret_cast<const uint32_t *>(&p);
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+};
+template <> struct Lane<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void unpack(uint4 r, float (&v)[4]) {
+        v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y);
+        v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[4]) {
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    }
+};
+
+template <typename T, int DV>
+__global__ void __launch_bounds__(kThreads)
+output_gate_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ o, const T *__restrict__ g,
+                       const float *__restrict__ weight, float eps, T *__restrict__ d_o, T *__restrict__ d_g,
+                       float *__restrict__ part, long long rows) {
+    using L = Lane<T>;
+    constexpr int N = L::N, LPR = DV / N, RPW = 32 / LPR, WARPS = kThreads / 32;
+    __shared__ float acc[WARPS][DV];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR, at = lane % LPR;
+    const long long groups = (rows + RPW - 1) / RPW, step = (long long)gridDim.x * WARPS * kUnroll;
+    float wt[N], aw[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        wt[e] = __ldg(weight + at * N + e);
+        aw[e] = 0.f;
+    }
+    for (long long g0 = ((long long)blockIdx.x * WARPS + warp) * kUnroll; g0 < groups; g0 += step) {
+        uint4 ro[kUnroll], rg[kUnroll], rd[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const long long row = (g0 + u) * RPW + sub;
+            const size_t off = (size_t)row * LPR + at;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            const bool in = row < rows;
+            ro[u] = in ? __ldcs(reinterpret_cast<const uint4 *>(o) + off) : zero;
+            rd[u] = in ? __ldcs(reinterpret_cast<const uint4 *>(dy) + off) : zero;
+            rg[u] = in ? __ldcs(reinterpret_cast<const uint4 *>(g) + off) : zero;
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const long long row = (g0 + u) * RPW + sub;
+            float n[N], s[N], t[N];
+            L::unpack(ro[u], n);
+            L::unpack(rg[u], s);
+            L::unpack(rd[u], t);
+            // both sums in one pass over the row: mean(t n) = rstd * mean(t o)
+            float ss = 0.f, dot = 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                s[e] = __fdividef(1.f, 1.f + __expf(-s[e]));
+                ss = fmaf(n[e], n[e], ss);
+                dot = fmaf(t[e] * wt[e] * s[e], n[e], dot);
+            }
+#pragma unroll
+            for (int m = LPR / 2; m > 0; m >>= 1) {
+                ss += __shfl_xor_sync(0xffffffffu, ss, m);
+                dot += __shfl_xor_sync(0xffffffffu, dot, m);
+            }
+            const float rstd = rsqrtf(ss * (1.f / DV) + eps), mean = dot * rstd * (1.f / DV);
+            float x[N], y[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                n[e] *= rstd;
+                const float ds = t[e] * s[e];
+                aw[e] = fmaf(ds, n[e], aw[e]);
+                const float dn = ds * wt[e];
+                x[e] = rstd * (dn - n[e] * mean);
+                y[e] = dn * n[e] * (1.f - s[e]);
+            }
+            if (row < rows) {
+                const size_t off = (size_t)row * LPR + at;
+                reinterpret_cast<uint4 *>(d_o)[off] = L::pack(x);
+                reinterpret_cast<uint4 *>(d_g)[off] = L::pack(y);
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+#pragma unroll
+        for (int m = LPR; m < 32; m <<= 1) aw[e] += __shfl_xor_sync(0xffffffffu, aw[e], m);
+        if (sub == 0) acc[warp][at * N + e] = aw[e];
+    }
+    __syncthreads();
+    if (threadIdx.x < DV) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) s += acc[i][threadIdx.x];
+        part[(size_t)blockIdx.x * DV + threadIdx.x] = s;
+    }
+}
+
+template <typename T> int grid_for(long long rows, int dv) {
+    const int per = 32 / (dv / Lane<T>::N) * (kThreads / 32) * kUnroll;     // rows per CTA and iteration
+    const long long need = (rows + per - 1) / per;
+    return (int)(need < kMaxGrid ? need : kMaxGrid);
+}
+
+template <typename T, int DV>
+cudaError_t launch_typed(const void *dy, const void *o, const void *g, const float *weight, float eps, void *d_o,
+                         void *d_g, float *part, long long rows, int grid, cudaStream_t st) {
+    output_gate_bwd_kernel<T, DV><<<grid, kThreads, 0, st>>>(
+        static_cast<const T *>(dy), static_cast<const T *>(o), static_cast<const T *>(g), weight, eps,
+        static_cast<T *>(d_o), static_cast<T *>(d_g), part, rows);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t output_gate_bwd_workspace_bytes(int dv) { return (size_t)kMaxGrid * dv * sizeof(float); }
+
+cudaError_t launch_output_gate_bwd(const void *dy, const void *o, const void *g, const float *weight, float eps,
+                                   void *d_o, void *d_g, float *dweight, float *workspace, long long rows, int dv,
+                                   gdn2_dtype dt, cudaStream_t st) {
+    const int grid = dt == GDN2_BF16 ? grid_for<bf16>(rows, dv) : grid_for<float>(rows, dv);
+    float *part = grid == 1 ? dweight : workspace;          // one CTA's sums are the result
+    cudaError_t e;
+    if (dt == GDN2_BF16)
+        e = dv == 128 ? launch_typed<bf16, 128>(dy, o, g, weight, eps, d_o, d_g, part, rows, grid, st)
+                      : launch_typed<bf16, 64>(dy, o, g, weight, eps, d_o, d_g, part, rows, grid, st);
+    else
+        e = dv == 128 ? launch_typed<float, 128>(dy, o, g, weight, eps, d_o, d_g, part, rows, grid, st)
+                      : launch_typed<float, 64>(dy, o, g, weight, eps, d_o, d_g, part, rows, grid, st);
+    if (e != cudaSuccess || grid == 1) return e;
+    return launch_reduce_parts(workspace, grid, dv, dv, dweight, nullptr, st);
+}
+
+}  // namespace gdn2

@@ -29,6 +29,7 @@
  *     b, w) and states are always FP32.  Accumulation is FP32.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
  *     Calls are asynchronous on that stream and never synchronise the device.
+ *     Index tensors (cu_seqlens, slots, keep, src, dst) need 4-byte alignment only.
  *   - Supported head sizes: d_k, d_v in {64, 128}.  Other sizes return
  *     GDN2_ERR_UNSUPPORTED.
  *   - Preconditions (documented, not checked on the device): 0 <= alpha <= 1;
@@ -216,6 +217,89 @@ gdn2_status gdn2_output_gate(const void *o, const void *g, const float *weight, 
                              int B, int T, int H, int d_v, gdn2_dtype dt, void *stream);
 
 /*
+ * Output epilogue's gradient.  With rstd = 1 / sqrt(mean_j(o_j^2) + eps), n = o rstd
+ * and s = sigmoid(g), per (token, head) row, t = dy weight s:
+ *   do = rstd (t - n mean_j(t n)),  dg = dy n weight s (1 - s),
+ *   dweight = sum over rows of dy n s.
+ *
+ *   dy, o, g   [B][T][H][d_v]  dt     read (o, g, weight, eps as in the forward call)
+ *   d_o, d_g   [B][T][H][d_v]  dt     written
+ *   dweight    [d_v]           float  written (not added to)
+ *   workspace  DEVICE, caller-owned, 16-byte aligned, at least
+ *              gdn2_output_gate_bwd_workspace_size(d_v) bytes; contents on entry do
+ *              not matter
+ *
+ * d_v 64 or 128.  FP32 arithmetic; dweight is summed in a fixed order (the same
+ * inputs give the same bits).  No output may overlap an input, another output or
+ * the workspace.  B = 0, T = 0 or H = 0 writes dweight = 0.
+ */
+gdn2_status gdn2_output_gate_bwd(const void *dy, const void *o, const void *g, const float *weight, float eps,
+                                 void *d_o, void *d_g, float *dweight, void *workspace, size_t workspace_bytes,
+                                 int B, int T, int H, int d_v, gdn2_dtype dt, void *stream);
+
+/* Bytes of workspace gdn2_output_gate_bwd needs (0 for an unsupported d_v). */
+size_t gdn2_output_gate_bwd_workspace_size(int d_v);
+
+/*
+ * The norm in front of a block, with the residual addition that ends the block
+ * before it (no counterpart in the paper, which names neither the layer's input
+ * norm nor its residual path; the usual pre-norm form).  Per row of D channels:
+ *   h = x + scale * dropout(r),   rstd = 1 / sqrt(mean_j(h_j^2) + eps),   y = h * rstd * weight
+ * y is computed from h before h is rounded to its type.
+ *
+ *   x          [rows][D]  stream_dt   read (the residual stream)
+ *   r          [rows][D]  dt          read (the branch: the previous block's output); NULL: h = x,
+ *                                     and scale, h must be NULL, p 0
+ *   weight     [D]        float       read
+ *   scale      [D]        float       read (residual scale); NULL means 1
+ *   p, rng                            dropout of r.  Element (row, c) is kept and scaled by
+ *              1 / (1 - p) where word c % 4 of Philox4x32-10 at counter (c / 4, row,
+ *              offset low, offset high) under key (seed low, seed high) is at least
+ *              floor(p 2^32), else 0.  rng: DEVICE, 8-byte aligned, two uint64 (seed,
+ *              offset), read by the kernel (a captured graph draws a new mask when the
+ *              program changes it); a call per step and layer needs an offset of its
+ *              own.  0 <= p < 1; p = 0 reads no rng and it may be NULL.
+ *   h          [rows][D]  stream_dt   written; may be x exactly (in place)
+ *   y          [rows][D]  dt          written; may be r exactly
+ *   rstd       [rows]     float       written (for the gradient)
+ *
+ * Types: stream_dt, dt both BF16, both FP32, or an FP32 stream with a BF16 branch.
+ * D from 1 to 16384 (multiples of 8 run vectorised).  rows = 0 is a no-op.
+ */
+gdn2_status gdn2_residual_norm(const void *x, const void *r, const float *weight, const float *scale, double p,
+                               const uint64_t *rng, float eps, void *h, void *y, float *rstd, int rows, int D,
+                               gdn2_dtype stream_dt, gdn2_dtype dt, void *stream);
+
+/*
+ * Its gradient, from the stored h and rstd.  With n = h rstd and t = weight dy:
+ *   dx = rstd (t - n mean_j(t n)) + dh,   dr = dropout(scale * dx) with the forward's mask,
+ *   dweight = sum over rows of dy n,      dscale = sum over rows of dx dropout(r).
+ *
+ *   dy         [rows][D]  dt          read
+ *   h, rstd                           read (the forward's outputs; h = x where it had no r)
+ *   dh         [rows][D]  stream_dt   read (gradient of h from later uses); NULL means zero
+ *   r, scale, p, rng                  as in the forward call; r is read for dscale only
+ *   dx         [rows][D]  stream_dt   written; may be dh exactly
+ *   dr         [rows][D]  dt          written; may be NULL (no branch, or dr = dx wanted as is)
+ *   dweight    [D]        float       written (not added to)
+ *   dscale     [D]        float       written; may be NULL; needs r and scale
+ *   workspace  DEVICE, caller-owned, 16-byte aligned, at least
+ *              gdn2_residual_norm_bwd_workspace_size(rows, D) bytes; contents on entry
+ *              do not matter
+ *
+ * FP32 arithmetic; dweight and dscale are summed in a fixed order (the same inputs
+ * give the same bits).  rows = 0 writes dweight = dscale = 0.
+ */
+gdn2_status gdn2_residual_norm_bwd(const void *dy, const void *h, const float *rstd, const float *weight,
+                                   const void *dh, const void *r, const float *scale, double p,
+                                   const uint64_t *rng, void *dx, void *dr, float *dweight, float *dscale,
+                                   void *workspace, size_t workspace_bytes, int rows, int D,
+                                   gdn2_dtype stream_dt, gdn2_dtype dt, void *stream);
+
+/* Bytes of workspace gdn2_residual_norm_bwd needs (0 for rows <= 0 or an unsupported D). */
+size_t gdn2_residual_norm_bwd_workspace_size(int rows, int D);
+
+/*
  * Chunkwise backward ("Token processing and parallel training": training goes
  * through the chunkwise form, so its gradient carries the channel-wise decay and
  * the separate erase and write gates through every per-block factor).  Computes
@@ -301,6 +385,76 @@ gdn2_status gdn2_recurrent_step(const void *q, const void *k, const void *v,
                                 int B, int H, int d_k, int d_v,
                                 gdn2_dtype dt, void *stream);
 
+/*
+ * The recurrent mode over a cache of states, for serving: N sequences, each with a
+ * slot of the cache and the next few tokens (one while decoding; several while
+ * drafts are verified or a short prompt is appended).  Per sequence: start from
+ * pool[slots[n]], run its tokens in order as gdn2_recurrent_step does, write every
+ * token's output, and store the state after its first keep[n] tokens back.
+ *
+ *   q, k      [T_total][H][d_k]  dt      read (sequence n is rows cu_seqlens[n] ..
+ *   v         [T_total][H][d_v]  dt      cu_seqlens[n+1] - 1 of every token tensor)
+ *   alpha, b  [T_total][H][d_k]  float   read
+ *   w         [T_total][H][d_v]  float   read
+ *   pool      [n_slots][H][d_k][d_v] float   read and written at the named slots
+ *   slots     [N] int32       DEVICE     read.  A slot outside [0, n_slots) (-1 for padding in
+ *                                        a batch of fixed size): the sequence's output rows
+ *                                        are set to zero and no state is touched.
+ *   cu_seqlens [N + 1] int32  DEVICE     read, clamped into [0, T_total]; NULL: one token per
+ *                                        sequence (T_total must be N).  Rows of o behind the
+ *                                        last sequence stay as they were, and a sequence
+ *                                        without tokens leaves its state as it is.
+ *   keep      [N] int32       DEVICE     read, clamped into [0, tokens of the sequence]; NULL:
+ *                                        all tokens.  0 leaves the state as it is.
+ *   g, weight, eps                       the output epilogue of gdn2_output_gate applied to o
+ *                                        before it is rounded (g [T_total][H][d_v] dt, weight
+ *                                        [d_v] float); both NULL: none
+ *   o         [T_total][H][d_v]  dt      written
+ *
+ * A slot may be named by several sequences only where none of them writes it (keep 0:
+ * branches of drafts from one state).  Otherwise every sequence that names it is
+ * treated as one with no slot, and gdn2_device_error reports 0x10000.
+ * d_k, d_v in {64, 128}; the state crosses HBM once in each direction whatever the
+ * number of tokens.  N = 0, H = 0 or T_total = 0 is a no-op.  pool and o must not
+ * overlap anything else.
+ */
+gdn2_status gdn2_slot_steps(const void *q, const void *k, const void *v, const float *alpha, const float *b,
+                            const float *w, float *pool, const int32_t *slots, const int32_t *cu_seqlens,
+                            const int32_t *keep, const void *g, const float *weight, float eps, void *o,
+                            int N, int T_total, int H, int n_slots, int d_k, int d_v, gdn2_dtype dt, void *stream);
+
+/*
+ * gdn2_slot_steps from BF16 pre-activation logits, with the input preparation of
+ * gdn2_chunk_fwd_logits inside the kernel (FP32, nothing rounded on the way): the
+ * step that continues a sequence prefilled from logits.  xq, xk, xa, xb are d_k
+ * wide, xv, xw d_v wide; d_k, d_v in {64, 128}; g and o BF16.
+ */
+gdn2_status gdn2_slot_steps_logits(const void *xq, const void *xk, const void *xv, const void *xa, const void *xb,
+                                   const void *xw, float *pool, const int32_t *slots, const int32_t *cu_seqlens,
+                                   const int32_t *keep, const void *g, const float *weight, float eps, void *o,
+                                   int N, int T_total, int H, int n_slots, int d_k, int d_v, void *stream);
+
+/*
+ * Copies states between slots of a cache, in all its layers at once: for every pair i,
+ * dst_pool[l][dst[i]] becomes what src_pool[l][src[i]] was before the call, for every
+ * layer l.  One call forks a sequence (one source, several destinations), compacts
+ * (a list of moves), swaps (any permutation, cycles included), frees (src -1: the
+ * destination is zeroed), or carries states between the cache and a dense batch
+ * (two pools: start states for gdn2_chunk_fwd_varlen and its end states back).
+ *
+ *   src_pool  [layers][n_src][H][d_k][d_v] float   read
+ *   dst_pool  [layers][n_dst][H][d_k][d_v] float   written at the named slots; may be
+ *                                                  src_pool exactly (then n_src = n_dst)
+ *   src, dst  [n] int32  DEVICE   read.  A pair with src outside [-1, n_src) or dst outside
+ *                                 [0, n_dst) is skipped; of several pairs with one destination
+ *                                 the last counts.
+ *
+ * n at most 4096 (GDN2_ERR_UNSUPPORTED beyond); d_k, d_v in {64, 128}.  n = 0,
+ * layers = 0, H = 0 or n_dst = 0 is a no-op.
+ */
+gdn2_status gdn2_state_copy(const float *src_pool, float *dst_pool, const int32_t *src, const int32_t *dst, int n,
+                            int layers, int n_src, int n_dst, int H, int d_k, int d_v, void *stream);
+
 /* Human-readable name of a status code (static string). */
 const char *gdn2_status_string(gdn2_status s);
 
@@ -309,10 +463,11 @@ const char *gdn2_status_string(gdn2_status s);
 const char *gdn2_last_error(void);
 
 /* Device-side failure flag of the current device (synchronous; call between
- * launches).  *code = 0 when every kernel finished normally; nonzero when a
- * bounded wait inside a kernel gave up (the kernel then skipped its remaining
- * work, released its resources and returned; outputs of that call are
- * undefined).  clear != 0 resets the flag. */
+ * launches).  *code = 0 when every kernel finished normally.  Low 16 bits
+ * nonzero: a bounded wait inside a kernel gave up (the kernel then skipped its
+ * remaining work, released its resources and returned; outputs of that call are
+ * undefined).  0x10000: a gdn2_slot_steps call named one slot twice (see there).
+ * clear != 0 resets the flags. */
 gdn2_status gdn2_device_error(unsigned int *code, int clear);
 
 /* Test hook for the kernels' failure handling.  Every wait inside the
