@@ -6,14 +6,23 @@
 //
 // Memory-bound: the forward reads x and r once and writes h and y once, the
 // backward reads dy, h, dh (and r for the scale's gradient) and writes dx and dr.
-// One CTA holds one row at a time in registers, one 8-channel vector per thread
-// (two above 8,192 channels), and walks the rows with a stride of the grid, so
-// that weight and scale are read once per CTA and, in the backward, their
-// gradients accumulate in registers over the CTA's rows.  The next row's loads
-// are issued before the current row's reduction.  Rows whose width is no
-// multiple of 8 are not 16-byte aligned; they go by 4-channel groups of single
-// elements.
+// One CTA holds one row at a time, 8 channels a thread, and walks the rows with a
+// stride of the grid, so that weight and scale are read once per CTA and, in the
+// backward, their gradients accumulate in registers over the CTA's rows.  The next
+// rows arrive by asynchronous copies into shared memory.  What the layout has to
+// keep: a lane's access covers whole 32-byte sectors together with its neighbours'
+// (8 consecutive FP32 channels a lane cost 125 us where 4 cost 95, 16,384 x 2,048
+// backward with an FP32 stream), and only 32 to 96 KB an SM are in flight (deeper
+// rings were 5 to 15 % slower).  The dropout's integer work (about 80 instructions
+// per 8 channels) comes before the wait for a row's data.
+//
+// Measured on a B200, 16,384 x 2,048, residual scale and p = 0.1: forward, BF16,
+// 49.0 us = 5.48 TB/s (45.7 us without dropout); FP32 stream and BF16 branch 63.9 us
+// = 6.30 TB/s; backward, FP32 stream, 94.3 us = 6.40 TB/s (99 % of a copy's rate), BF16
+// 73.8 us = 5.46 TB/s, bound there by the mask's and the conversions' instructions.
+#include "async_copy.cuh"
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "philox.cuh"
 
 namespace gdn2 {
@@ -24,99 +33,228 @@ using bf16 = __nv_bfloat16;
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(bf16 x) { return __bfloat162float(x); }
 
-// One thread's V consecutive channels of a row, as loaded.
-template <typename T, bool ALIGNED> struct Frag;
-template <> struct Frag<bf16, true> {
-    static constexpr int V = 8;
-    uint4 raw;
-    __device__ __forceinline__ void load(const bf16 *row, int c, int D) {
-        raw = c < D ? __ldcs(reinterpret_cast<const uint4 *>(row + c)) : make_uint4(0, 0, 0, 0);
-    }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+// A vector: V consecutive channels of a row in one thread, as pairs.  Aligned rows (D a
+// multiple of 8) move as whole vectors of V sizeof(T) = 8 or 16 bytes; the lanes of a
+// warp then touch whole sectors of every tensor (8 FP32 channels a lane would leave
+// each access half of a sector).  Other rows go by single elements.
+template <typename TS, typename TB, bool AL> constexpr int vector_channels() {
+    return AL && sizeof(TS) + sizeof(TB) == 4 ? 8 : 4;
+}
+
+template <int BYTES> struct Raw;
+template <> struct Raw<16> { uint4 u; };
+template <> struct Raw<8> { uint2 u; };
+template <typename T, int V> using RawOf = Raw<V * (int)sizeof(T)>;
+
+__device__ __forceinline__ void widen(uint32_t u, Pair &v) {
+    v = pack2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+__device__ __forceinline__ void unpack(const Raw<16> &r, Pair (&v)[4]) {       // 8 BF16
+    widen(r.u.x, v[0]); widen(r.u.y, v[1]); widen(r.u.z, v[2]); widen(r.u.w, v[3]);
+}
+__device__ __forceinline__ void unpack(const Raw<8> &r, Pair (&v)[2]) {        // 4 BF16
+    widen(r.u.x, v[0]); widen(r.u.y, v[1]);
+}
+__device__ __forceinline__ void unpack(const Raw<16> &r, Pair (&v)[2]) {       // 4 FP32
+    v[0] = pack2(__uint_as_float(r.u.x), __uint_as_float(r.u.y));
+    v[1] = pack2(__uint_as_float(r.u.z), __uint_as_float(r.u.w));
+}
+__device__ __forceinline__ uint32_t narrow(Pair v) {
+    float a, b;
+    unpack2(v, a, b);
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+__device__ __forceinline__ void pack(const Pair (&v)[4], Raw<16> &r) {
+    r.u = make_uint4(narrow(v[0]), narrow(v[1]), narrow(v[2]), narrow(v[3]));
+}
+__device__ __forceinline__ void pack(const Pair (&v)[2], Raw<8> &r) { r.u = make_uint2(narrow(v[0]), narrow(v[1])); }
+__device__ __forceinline__ void pack(const Pair (&v)[2], Raw<16> &r) {
+    float a, b, c, d;
+    unpack2(v[0], a, b);
+    unpack2(v[1], c, d);
+    r.u = make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+}
+
+// A pair of FP32 values by its mask word.
+__device__ __forceinline__ Pair mask2(Pair v, uint32_t m) {
+    float a, b;
+    unpack2(v, a, b);
+    return pack2(__uint_as_float(__float_as_uint(a) & __byte_perm(m, 0, 0x1010)),
+                 __uint_as_float(__float_as_uint(b) & __byte_perm(m, 0, 0x3232)));
+}
+
+// Masks V values of type T (one word of m per pair).
+__device__ __forceinline__ void mask(Raw<16> &r, const uint32_t (&m)[4]) { r.u.x &= m[0]; r.u.y &= m[1]; r.u.z &= m[2]; r.u.w &= m[3]; }
+__device__ __forceinline__ void mask(Raw<8> &r, const uint32_t (&m)[2]) { r.u.x &= m[0]; r.u.y &= m[1]; }
+__device__ __forceinline__ void mask(Raw<16> &r, const uint32_t (&m)[2]) {
+    r.u.x &= __byte_perm(m[0], 0, 0x1010); r.u.y &= __byte_perm(m[0], 0, 0x3232);
+    r.u.z &= __byte_perm(m[1], 0, 0x1010); r.u.w &= __byte_perm(m[1], 0, 0x3232);
+}
+
+template <typename T, bool AL, int V> __device__ __forceinline__ void load(const T *p, int left, RawOf<T, V> &r, Pair (&v)[V / 2]) {
+    if constexpr (AL) {
+        using U = decltype(r.u);
+        if (left > 0) r.u = __ldcs(reinterpret_cast<const U *>(p));
+    } else {
+        float x[V];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[2 * e] = __uint_as_float(u[e] << 16);
-            v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+        for (int e = 0; e < V; ++e) x[e] = e < left ? to_float(__ldcs(p + e)) : 0.f;
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) v[e] = pack2(x[2 * e], x[2 * e + 1]);
+    }
+}
+template <typename T, bool AL, int V>
+__device__ __forceinline__ void store(T *p, int left, const Pair (&v)[V / 2], const uint32_t (*m)[V / 2] = nullptr) {
+    if constexpr (AL) {
+        RawOf<T, V> r;
+        pack(v, r);
+        if (m) mask(r, *m);
+        if (left > 0) *reinterpret_cast<decltype(r.u) *>(p) = r.u;
+    } else {
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+            float a, b;
+            unpack2(m ? mask2(v[e], (*m)[e]) : v[e], a, b);
+            if (2 * e < left) Elem<T>::store(p + 2 * e, a);
+            if (2 * e + 1 < left) Elem<T>::store(p + 2 * e + 1, b);
         }
     }
-    static __device__ __forceinline__ void store(bf16 *row, int c, int D, const float (&v)[8]) {
-        if (c >= D) return;
-        uint32_t u[4];
+}
+
+// Rows of one tensor on their way to a thread, VPT vectors of each row.  S = 0: in
+// registers, one row ahead.  S > 0: asynchronous copies into shared memory, S rows
+// ahead; a thread reads only what it copied itself, so waiting for its own copies is all
+// the synchronisation there is.  A thread's vector j of a stage lies `at` + j vectors
+// of MAXT threads into the stage.
+template <typename T, bool AL, int V, int VPT, int MAXT, int S> struct Rows {
+    static constexpr int B = V * (int)sizeof(T), BYTES = VPT * MAXT * B;       // of a stage
+    RawOf<T, V> raw[S ? 1 : VPT];
+    Pair val[AL || S ? 1 : VPT][V / 2];
+    const T *base;
+    // Channels past the row's end are zero: set here once, never copied over.
+    __device__ __forceinline__ void init(const T *p, int left, uint32_t at, uint32_t stage_bytes) {
+        base = p;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-            u[e] = *reinterpret_cast<const uint32_t *>(&p);
+        for (int j = 0; j < VPT; ++j) {
+            if constexpr (S > 0) {
+                if (left <= j * (int)blockDim.x * V)
+                    for (int i = 0; i < S; ++i)
+                        zero_shared<B>(at + i * stage_bytes + threadIdx.x * B + j * MAXT * B);
+            } else if constexpr (AL) {
+                raw[j] = {};
+            }
         }
-        *reinterpret_cast<uint4 *>(row + c) = make_uint4(u[0], u[1], u[2], u[3]);
     }
-};
-template <> struct Frag<float, true> {
-    static constexpr int V = 8;
-    float4 raw[2];
-    __device__ __forceinline__ void load(const float *row, int c, int D) {
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        raw[0] = c < D ? __ldcs(reinterpret_cast<const float4 *>(row + c)) : zero;
-        raw[1] = c < D ? __ldcs(reinterpret_cast<const float4 *>(row + c) + 1) : zero;
-    }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        v[0] = raw[0].x; v[1] = raw[0].y; v[2] = raw[0].z; v[3] = raw[0].w;
-        v[4] = raw[1].x; v[5] = raw[1].y; v[6] = raw[1].z; v[7] = raw[1].w;
-    }
-    static __device__ __forceinline__ void store(float *row, int c, int D, const float (&v)[8]) {
-        if (c >= D) return;
-        reinterpret_cast<float4 *>(row + c)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4 *>(row + c)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    }
-};
-template <typename T> struct Frag<T, false> {
-    static constexpr int V = 4;
-    float raw[4];
-    __device__ __forceinline__ void load(const T *row, int c, int D) {
+    // `e`: the element offset of the thread's first vector; `left`: channels from there to the row's end
+    __device__ __forceinline__ void fetch(size_t e, int left, uint32_t at) {
+        if (!base) return;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) raw[e] = c + e < D ? to_float(__ldcs(row + c + e)) : 0.f;
+        for (int j = 0; j < VPT; ++j) {
+            const int skip = j * (int)blockDim.x * V;
+            if constexpr (S > 0) {
+                if (left > skip) copy_async<B>(at + threadIdx.x * B + j * MAXT * B, base + e + skip);
+            } else {
+                load<T, AL, V>(base + e + skip, left - skip, raw[j], val[AL ? 0 : j]);
+            }
+        }
     }
-    __device__ __forceinline__ void get(float (&v)[4]) const {
+    __device__ __forceinline__ void read(int j, uint32_t at, Pair (&v)[V / 2],
+                                         const uint32_t (*m)[V / 2] = nullptr) {
+        if constexpr (AL) {
+            RawOf<T, V> r;
+            if constexpr (S > 0)
+                load_shared(at + threadIdx.x * B + j * MAXT * B, r.u);
+            else
+                r = raw[j];
+            if (m) mask(r, *m);
+            unpack(r, v);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = raw[e];
-    }
-    static __device__ __forceinline__ void store(T *row, int c, int D, const float (&v)[4]) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (c + e < D) Elem<T>::store(row + c + e, v[e]);
+            for (int e = 0; e < V / 2; ++e) v[e] = m ? mask2(val[j][e], (*m)[e]) : val[j][e];
+        }
     }
 };
 
-template <int V> __device__ __forceinline__ void load_channels(const float *p, int c, int D, float fill, float (&v)[V]) {
+// A [D] vector's channels of one thread, times `factor`; `fill` where p is null.  In
+// registers, or (SHARED: CTAs of 1,024 threads, which have 64 registers each) in the
+// thread's own part of shared memory.
+template <int V, int VPT, int MAXT, bool SHARED> struct Channels {
+    Pair reg[SHARED ? 1 : VPT][V / 2];
+    uint32_t at;
+    __device__ __forceinline__ void init(const float *p, uint32_t smem, int D, float fill, float factor) {
+        at = smem + threadIdx.x * 16;
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = p && c + e < D ? __ldg(p + c + e) : fill;
-}
+        for (int j = 0; j < VPT; ++j) {
+            const int c = (j * (int)blockDim.x + (int)threadIdx.x) * V;
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const Pair x = pack2((p && c + 2 * i < D ? __ldg(p + c + 2 * i) : fill) * factor,
+                                     (p && c + 2 * i + 1 < D ? __ldg(p + c + 2 * i + 1) : fill) * factor);
+                if constexpr (SHARED)
+                    store_shared(at + (j * V / 4 + i / 2) * MAXT * 16 + i % 2 * 8, x.v);
+                else
+                    reg[j][i] = x;
+            }
+        }
+    }
+    __device__ __forceinline__ void get(int j, Pair (&v)[V / 2]) const {
+#pragma unroll
+        for (int i = 0; i < V / 2; i += 2) {
+            if constexpr (SHARED) {
+                load_shared(at + (j * V / 4 + i / 2) * MAXT * 16, v[i].v, v[i + 1].v);
+            } else {
+                v[i] = reg[j][i];
+                v[i + 1] = reg[j][i + 1];
+            }
+        }
+    }
+};
 
 // Sum over the CTA, the same bits in every thread.  `buf` alternates between two
 // halves from one call to the next, so one barrier per call is enough.
-__device__ __forceinline__ float cta_sum(float x, float *buf) {
+template <int MAXT> __device__ __forceinline__ float cta_sum(float x, float *buf) {
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-    const int warps = blockDim.x >> 5;
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
     if (warps == 1) return x;
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+    if (lane == 0) buf[threadIdx.x >> 5] = x;
     __syncthreads();
-    float s = 0.f;
-    for (int i = 0; i < warps; ++i) s += buf[i];
-    return s;
+    x = (lane & (MAXT / 32 - 1)) < warps ? buf[lane & (MAXT / 32 - 1)] : 0.f;
+#pragma unroll
+    for (int m = MAXT / 64; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    return x;
 }
 
-// dropout of V channels starting at column c (a multiple of 4)
-template <int V>
-__device__ __forceinline__ void drop(float (&v)[V], const Dropout &dp, uint2 key, uint2 offset, int row, int c) {
+// Which channels of a thread's vectors a row keeps: one word per pair, its low half ones
+// for the first channel and its high half for the second.  Two BF16 values are masked
+// by one operation, and a dropped value leaves nothing, whatever it was.
+template <int V, int VPT> struct Keep {
+    philox::Lane lane[VPT * V / 4];
+    uint32_t m[VPT][V / 2];
+    __device__ __forceinline__ void init(const Dropout &dp, uint2 key, uint2 offset, int c0) {
+        if (dp.rng)
 #pragma unroll
-    for (int q = 0; q < V; q += 4) {
-        const uint4 w = philox4x32(make_uint4((uint32_t)(c + q) >> 2, (uint32_t)row, offset.x, offset.y), key);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            for (int q = 0; q < VPT * V / 4; ++q) {
+                const int c = c0 + q / (V / 4) * (int)blockDim.x * V + q % (V / 4) * 4;
+                lane[q] = philox::lane_for((uint32_t)c >> 2, key, offset);
+            }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[q + e] = u[e] >= dp.threshold ? v[q + e] * dp.inv_keep : 0.f;
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) m[j][i] = 0xffffffffu;
     }
-}
+    __device__ __forceinline__ void draw(const Dropout &dp, uint2 key, uint2 offset, int row) {
+        const philox::Row r = philox::row_for((uint32_t)row, key, offset);
+#pragma unroll
+        for (int q = 0; q < VPT * V / 4; ++q) {
+            const uint4 w = philox::words(lane[q], r, key);
+            uint32_t *to = m[q / (V / 4)] + q % (V / 4) * 2;
+            to[0] = (w.x >= dp.threshold ? 0xffffu : 0u) | (w.y >= dp.threshold ? 0xffff0000u : 0u);
+            to[1] = (w.z >= dp.threshold ? 0xffffu : 0u) | (w.w >= dp.threshold ? 0xffff0000u : 0u);
+        }
+    }
+};
 
 __device__ __forceinline__ void rng_words(const Dropout &dp, uint2 &key, uint2 &offset) {
     key = offset = make_uint2(0u, 0u);
@@ -126,64 +264,81 @@ __device__ __forceinline__ void rng_words(const Dropout &dp, uint2 &key, uint2 &
     offset = make_uint2((uint32_t)o, (uint32_t)(o >> 32));
 }
 
-template <typename TS, typename TB, bool ALIGNED, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT)
+template <typename TS, typename TB, bool AL, int VPT, int MAXT, int S>
+__global__ void __launch_bounds__(MAXT, 1024 / MAXT)
 residual_norm_kernel(const TS *x, const TB *r, const float *__restrict__ weight, const float *__restrict__ scale,
                      Dropout dp, float eps, TS *h, TB *y, float *__restrict__ rstd, int rows, int D) {
-    using FS = Frag<TS, ALIGNED>;
-    using FB = Frag<TB, ALIGNED>;
-    constexpr int V = FS::V;
+    constexpr int V = vector_channels<TS, TB, AL>(), P = V / 2;
+    using RS = Rows<TS, AL, V, VPT, MAXT, S>;
+    using RB = Rows<TB, AL, V, VPT, MAXT, S>;
+    constexpr uint32_t kStage = RS::BYTES + RB::BYTES;
+    extern __shared__ uint4 ring[];
     __shared__ float red[2][32];
+    const uint32_t ring0 = smem_address(ring);
     uint2 key, offset;
     rng_words(dp, key, offset);
-    float wt[VPT][V], sc[VPT][V];
-    FS fx[VPT];
-    FB fr[VPT];
+    const int grid = gridDim.x, c0 = threadIdx.x * V, left = D - c0;
+    RS rx;
+    RB rr;
+    rx.init(x, left, ring0, kStage);
+    rr.init(r, left, ring0 + RS::BYTES, kStage);
+    const size_t step = (size_t)grid * D;
+    int row = blockIdx.x, ahead = row;                  // the row in hand and the next one to fetch
+    size_t e = (size_t)row * D + c0, e_ahead = e;
+    auto fetch = [&](uint32_t at) {
+        if (ahead < rows) {
+            rx.fetch(e_ahead, left, at);
+            rr.fetch(e_ahead, left, at + RS::BYTES);
+        }
+        ahead = ahead < rows ? ahead + grid : ahead;
+        e_ahead += step;
+        if constexpr (S > 0) copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < (S ? S : 1); ++i) fetch(ring0 + i * kStage);
+    Channels<V, VPT, MAXT, false> wt, sc;
+    wt.init(weight, 0, D, 0.f, 1.f);
+    sc.init(scale, 0, D, 1.f, dp.inv_keep);
+    Keep<V, VPT> keep;
+    keep.init(dp, key, offset, c0);
     const float inv_d = 1.f / (float)D;
-    int row = blockIdx.x;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int c = (j * blockDim.x + threadIdx.x) * V;
-        load_channels<V>(weight, c, D, 0.f, wt[j]);
-        load_channels<V>(scale, c, D, 1.f, sc[j]);
-        fx[j].load(x + (size_t)row * D, c, D);
-        if (r) fr[j].load(r + (size_t)row * D, c, D);
-    }
-    for (int it = 0; row < rows; row += gridDim.x, ++it) {
-        float hv[VPT][V], ss = 0.f;
+    uint32_t at = ring0;
+    for (int it = 0; row < rows; row += grid, it ^= 1) {
+        if (dp.rng) keep.draw(dp, key, offset, row);    // before the wait: needs no data
+        if constexpr (S > 0) copy_wait<S ? S - 1 : 0>();
+        Pair hv[VPT][P], ss2 = pack2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = (j * blockDim.x + threadIdx.x) * V;
-            fx[j].get(hv[j]);
+            rx.read(j, at, hv[j]);
             if (r) {
-                float b[V];
-                fr[j].get(b);
-                if (dp.rng) drop<V>(b, dp, key, offset, row, c);
+                Pair b[P], s[P];
+                rr.read(j, at + RS::BYTES, b, &keep.m[j]);
+                sc.get(j, s);
 #pragma unroll
-                for (int e = 0; e < V; ++e) hv[j][e] = fmaf(b[e], sc[j][e], hv[j][e]);
+                for (int i = 0; i < P; ++i) hv[j][i] = fma2(b[i], s[i], hv[j][i]);
             }
 #pragma unroll
-            for (int e = 0; e < V; ++e) ss = fmaf(hv[j][e], hv[j][e], ss);
+            for (int i = 0; i < P; ++i) ss2 = fma2(hv[j][i], hv[j][i], ss2);
         }
-        if (row + (long long)gridDim.x < rows) {
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int c = (j * blockDim.x + threadIdx.x) * V;
-                fx[j].load(x + (size_t)(row + gridDim.x) * D, c, D);
-                if (r) fr[j].load(r + (size_t)(row + gridDim.x) * D, c, D);
-            }
-        }
-        const float rs = rsqrtf(cta_sum(ss, red[it & 1]) * inv_d + eps);
+        fetch(at);                                  // this thread's part of the stage has been read
+        if constexpr (S > 0) at = at == ring0 + (S - 1) * kStage ? ring0 : at + kStage;
+        float s0, s1;
+        unpack2(ss2, s0, s1);
+        const float rs = rsqrtf(cta_sum<MAXT>(s0 + s1, red[it]) * inv_d + eps);
         if (threadIdx.x == 0) rstd[row] = rs;
+        const Pair rs2 = pack2(rs, rs);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = (j * blockDim.x + threadIdx.x) * V;
-            if (h) FS::store(h + (size_t)row * D, c, D, hv[j]);
+            const int skip = j * (int)blockDim.x * V;
+            if (h) store<TS, AL, V>(h + e + skip, left - skip, hv[j]);
+            Pair w[P];
+            wt.get(j, w);
 #pragma unroll
-            for (int e = 0; e < V; ++e) hv[j][e] = hv[j][e] * rs * wt[j][e];
-            FB::store(y + (size_t)row * D, c, D, hv[j]);
+            for (int i = 0; i < P; ++i) hv[j][i] = mul2(mul2(hv[j][i], rs2), w[i]);
+            store<TB, AL, V>(y + e + skip, left - skip, hv[j]);
         }
-        if (row > rows - (int)gridDim.x) break;      // keeps row + gridDim.x below 2^31
+        e += step;
+        if (row >= rows - grid) break;              // row + grid may pass 2^31
     }
 }
 
@@ -193,104 +348,133 @@ residual_norm_kernel(const TS *x, const TB *r, const float *__restrict__ weight,
 // A CTA adds its rows' shares of the two sums in registers and writes them to its
 // row of `part` ([gridDim][1 or 2][D]); reduce_parts_kernel adds those in a fixed
 // order, so the result does not change from call to call.
-template <typename TS, typename TB, bool ALIGNED, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT)
+template <typename TS, typename TB, bool AL, int VPT, int MAXT, int S>
+__global__ void __launch_bounds__(MAXT, MAXT <= 512 ? 512 / MAXT : 1)
 residual_norm_bwd_kernel(const TB *__restrict__ dy, const TS *__restrict__ h, const float *__restrict__ rstd,
                          const float *__restrict__ weight, const TS *dh, const TB *__restrict__ r,
                          const float *__restrict__ scale, Dropout dp, TS *dx, TB *__restrict__ dr,
                          float *__restrict__ part, int rows, int D) {
-    using FS = Frag<TS, ALIGNED>;
-    using FB = Frag<TB, ALIGNED>;
-    constexpr int V = FS::V;
+    constexpr int V = vector_channels<TS, TB, AL>(), P = V / 2;
+    using RS = Rows<TS, AL, V, VPT, MAXT, S>;
+    using RB = Rows<TB, AL, V, VPT, MAXT, S>;
+    using C = Channels<V, VPT, MAXT, (MAXT > 512 && S > 0)>;
+    constexpr uint32_t kDh = RS::BYTES, kDy = 2 * RS::BYTES, kR = kDy + RB::BYTES, kStage = kR + RB::BYTES;
+    extern __shared__ uint4 ring[];
     __shared__ float red[2][32];
+    cudaTriggerProgrammaticLaunchCompletion();       // the sums' launch may be set up; it waits for this grid's end
+    const uint32_t ring0 = smem_address(ring);
     uint2 key, offset;
     rng_words(dp, key, offset);
-    float wt[VPT][V], sc[VPT][V], aw[VPT][V], as[VPT][V];
-    FB fdy[VPT], fr[VPT];
-    FS fh[VPT], fdh[VPT];
-    const float inv_d = 1.f / (float)D;
-    auto load_row = [&](int row) {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int c = (j * blockDim.x + threadIdx.x) * V;
-            fdy[j].load(dy + (size_t)row * D, c, D);
-            fh[j].load(h + (size_t)row * D, c, D);
-            if (dh) fdh[j].load(dh + (size_t)row * D, c, D);
-            if (r) fr[j].load(r + (size_t)row * D, c, D);
+    RB rdy, rr;
+    RS rh, rdh;
+    const int grid = gridDim.x, c0 = threadIdx.x * V, left = D - c0;
+    rdy.init(dy, left, ring0 + kDy, kStage);
+    rr.init(r, left, ring0 + kR, kStage);
+    rh.init(h, left, ring0, kStage);
+    rdh.init(dh, left, ring0 + kDh, kStage);
+    const size_t step = (size_t)grid * D;
+    int row = blockIdx.x, ahead = row;                  // the row in hand and the next one to fetch
+    size_t e = (size_t)row * D + c0, e_ahead = e;
+    auto fetch = [&](uint32_t at) {
+        if (ahead < rows) {
+            rdy.fetch(e_ahead, left, at + kDy);
+            rh.fetch(e_ahead, left, at);
+            rdh.fetch(e_ahead, left, at + kDh);
+            rr.fetch(e_ahead, left, at + kR);
         }
+        ahead = ahead < rows ? ahead + grid : ahead;
+        e_ahead += step;
+        if constexpr (S > 0) copy_commit();
     };
-    int row = blockIdx.x;
-    load_row(row);
+#pragma unroll
+    for (int i = 0; i < (S ? S : 1); ++i) fetch(ring0 + i * kStage);
     float rs_next = __ldg(rstd + row);
+    C wt, sc;
+    wt.init(weight, ring0 + S * kStage, D, 0.f, 1.f);
+    sc.init(scale, ring0 + S * kStage + VPT * MAXT * V * 4, D, 1.f, dp.inv_keep);
+    Pair aw[VPT][P], as[VPT][P];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int c = (j * blockDim.x + threadIdx.x) * V;
-        load_channels<V>(weight, c, D, 0.f, wt[j]);
-        load_channels<V>(scale, c, D, 1.f, sc[j]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) aw[j][e] = as[j][e] = 0.f;
+        for (int i = 0; i < P; ++i) aw[j][i] = as[j][i] = pack2(0.f, 0.f);
     }
-    for (int it = 0; row < rows; row += gridDim.x, ++it) {
+    Keep<V, VPT> keep;
+    keep.init(dp, key, offset, c0);
+    const float inv_d = 1.f / (float)D;
+    uint32_t at = ring0;
+    for (int it = 0; row < rows; row += grid, it ^= 1) {
+        if (dp.rng) keep.draw(dp, key, offset, row);    // before the wait: needs no data
         const float rs = rs_next;
-        float n[VPT][V], t[VPT][V], gx[VPT][V], b[VPT][V], dot = 0.f;
+        const Pair rs2 = pack2(rs, rs);
+        if constexpr (S > 0) copy_wait<S ? S - 1 : 0>();
+        Pair n[VPT][P], t[VPT][P], gx[VPT][P], b[VPT][P], dot2 = pack2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            fdy[j].get(t[j]);
-            fh[j].get(n[j]);
-            if (dh) fdh[j].get(gx[j]);
-            if (r) fr[j].get(b[j]);
+            rdy.read(j, at + kDy, t[j]);
+            rh.read(j, at, n[j]);
+            Pair w[P];
+            wt.get(j, w);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if (!dh) gx[j][e] = 0.f;
-                n[j][e] *= rs;
-                aw[j][e] = fmaf(t[j][e], n[j][e], aw[j][e]);
-                t[j][e] *= wt[j][e];
-                dot = fmaf(t[j][e], n[j][e], dot);
+            for (int i = 0; i < P; ++i) {
+                n[j][i] = mul2(n[j][i], rs2);
+                aw[j][i] = fma2(t[j][i], n[j][i], aw[j][i]);
+                t[j][i] = mul2(t[j][i], w[i]);
+                dot2 = fma2(t[j][i], n[j][i], dot2);
             }
         }
-        if (row + (long long)gridDim.x < rows) {
-            load_row(row + gridDim.x);
-            rs_next = __ldg(rstd + row + gridDim.x);
-        }
-        const float mean = cta_sum(dot, red[it & 1]) * inv_d;
+        const bool last = row >= rows - grid;
+        if (!last) rs_next = __ldg(rstd + row + grid);
+        float d0, d1;
+        unpack2(dot2, d0, d1);
+        const float mean = -cta_sum<MAXT>(d0 + d1, red[it]) * inv_d;
+        const Pair mean2 = pack2(mean, mean);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = (j * blockDim.x + threadIdx.x) * V;
-            float g[V];
+            if (dh) rdh.read(j, at + kDh, gx[j]);
+            if (r) rr.read(j, at + kR, b[j], &keep.m[j]);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                gx[j][e] = fmaf(rs, t[j][e] - n[j][e] * mean, gx[j][e]);
-                g[e] = gx[j][e];
+            for (int i = 0; i < P; ++i)
+                if (!dh) gx[j][i] = pack2(0.f, 0.f);
+        }
+        fetch(at);                                  // this thread's part of the stage has been read
+        if constexpr (S > 0) at = at == ring0 + (S - 1) * kStage ? ring0 : at + kStage;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int skip = j * (int)blockDim.x * V;
+#pragma unroll
+            for (int i = 0; i < P; ++i) gx[j][i] = fma2(rs2, fma2(n[j][i], mean2, t[j][i]), gx[j][i]);
+            store<TS, AL, V>(dx + e + skip, left - skip, gx[j]);
+            if (r) {                                // as is scaled by 1 / (1 - p) at the end
+#pragma unroll
+                for (int i = 0; i < P; ++i) as[j][i] = fma2(gx[j][i], b[j][i], as[j][i]);
             }
-            FS::store(dx + (size_t)row * D, c, D, gx[j]);
-            if (dr || r) {
-                float keep[V];
+            if (dr) {
+                Pair s[P];
+                sc.get(j, s);
 #pragma unroll
-                for (int e = 0; e < V; ++e) keep[e] = 1.f;
-                if (dp.rng) drop<V>(keep, dp, key, offset, row, c);      // 1 / (1 - p) or 0
-                if (r) {
-#pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        as[j][e] = keep[e] != 0.f ? fmaf(g[e] * keep[e], b[j][e], as[j][e]) : as[j][e];
-                }
-                if (dr) {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) g[e] = keep[e] != 0.f ? g[e] * sc[j][e] * keep[e] : 0.f;
-                    FB::store(dr + (size_t)row * D, c, D, g);
-                }
+                for (int i = 0; i < P; ++i) gx[j][i] = mul2(gx[j][i], s[i]);
+                store<TB, AL, V>(dr + e + skip, left - skip, gx[j], &keep.m[j]);
             }
         }
-        if (row > rows - (int)gridDim.x) break;
+        e += step;
+        if (last) break;                            // row + grid may pass 2^31
     }
     float *pw = part + (size_t)blockIdx.x * (r ? 2 : 1) * D;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int c = (j * blockDim.x + threadIdx.x) * V;
+        const int c = c0 + j * (int)blockDim.x * V;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            if (c + e < D) {
-                pw[c + e] = aw[j][e];
-                if (r) pw[D + c + e] = as[j][e];
+        for (int i = 0; i < P; ++i) {
+            float a0, a1, s0, s1;
+            unpack2(aw[j][i], a0, a1);
+            unpack2(as[j][i], s0, s1);
+            if (c + 2 * i < D) {
+                pw[c + 2 * i] = a0;
+                if (r) pw[D + c + 2 * i] = s0 * dp.inv_keep;
+            }
+            if (c + 2 * i + 1 < D) {
+                pw[c + 2 * i + 1] = a1;
+                if (r) pw[D + c + 2 * i + 1] = s1 * dp.inv_keep;
             }
         }
     }
@@ -303,6 +487,7 @@ __global__ void __launch_bounds__(1024)
 reduce_parts_kernel(const float *__restrict__ part, int G, int W, int D0, float *__restrict__ out0,
                     float *__restrict__ out1) {
     __shared__ float acc[32][33];
+    cudaGridDependencySynchronize();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.f;
     if (c < W)
@@ -326,35 +511,58 @@ int device_sms() {
     return sms;
 }
 
-int threads_for(int D, bool aligned, int vpt) {
-    const int per = (aligned ? 8 : 4) * vpt;
-    return ((D + per - 1) / per + 31) / 32 * 32;
+// How a width is split over a CTA: 8 channels a thread up to 8,192 (aligned, through the
+// shared-memory ring) or 4 up to 4,096 (not aligned); more channels a thread, in
+// registers, beyond.
+struct Split {
+    int threads;
+    bool aligned, wide;
+};
+Split split_for(int D) {
+    Split s{0, D % 8 == 0, false};
+    int per = s.aligned ? 8 : 4;
+    s.wide = D > per * 1024;
+    if (s.wide) per *= s.aligned ? 2 : 4;
+    s.threads = ((D + per - 1) / per + 31) / 32 * 32;
+    return s;
 }
 
-template <typename TS, typename TB, bool AL, int VPT>
-cudaError_t fwd_typed(const void *x, const void *r, const float *weight, const float *scale, const Dropout &dp,
-                      float eps, void *h, void *y, float *rstd, int rows, int D, cudaStream_t st) {
-    const int threads = threads_for(D, AL, VPT);
-    const int per_sm = threads >= 1024 ? 1 : 1024 / threads;
-    const long long cap = (long long)device_sms() * (per_sm > 32 ? 32 : per_sm);
-    const int grid = (int)(rows < cap ? rows : cap);
-    auto kernel = threads <= 256   ? residual_norm_kernel<TS, TB, AL, VPT, 256>
-                  : threads <= 512 ? residual_norm_kernel<TS, TB, AL, VPT, 512>
-                                   : residual_norm_kernel<TS, TB, AL, VPT, 1024>;
-    kernel<<<grid, threads, 0, st>>>(static_cast<const TS *>(x), static_cast<const TB *>(r), weight, scale, dp, eps,
-                                     static_cast<TS *>(h), static_cast<TB *>(y), rstd, rows, D);
+// CTAs per SM: 1,024 threads of the forward (64 registers each), 512 of the backward
+// (its two sums' accumulators take 128).
+int grid_for(int rows, int threads, int per_sm, int sms) {
+    const int ctas = threads >= per_sm ? 1 : per_sm / threads;
+    const long long cap = (long long)sms * ctas;
+    return (int)(rows < cap ? rows : cap);
+}
+
+// More than 48 KB, static shared memory included, needs an opt-in.
+template <typename K> cudaError_t allow_smem(K kernel, size_t bytes) {
+    return bytes > 46 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
+                             : cudaSuccess;
+}
+
+struct FwdArgs {
+    const void *x, *r;
+    const float *weight, *scale;
+    Dropout dp;
+    float eps;
+    void *h, *y;
+    float *rstd;
+    int rows, D;
+};
+
+template <typename TS, typename TB, bool AL, int VPT, int MAXT, bool RING>
+cudaError_t fwd_launch(const FwdArgs &a, int threads, cudaStream_t st) {
+    constexpr int bytes = VPT * vector_channels<TS, TB, AL>() * (int)(sizeof(TS) + sizeof(TB));
+    constexpr int S = RING ? 1 : 0;          // 32 to 64 KB in flight an SM; two rows ahead measured slower
+    auto kernel = residual_norm_kernel<TS, TB, AL, VPT, MAXT, S>;
+    const size_t smem = (size_t)MAXT * bytes * S;
+    const cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid_for(a.rows, threads, 1024, device_sms()), threads, smem, st>>>(
+        static_cast<const TS *>(a.x), static_cast<const TB *>(a.r), a.weight, a.scale, a.dp, a.eps,
+        static_cast<TS *>(a.h), static_cast<TB *>(a.y), a.rstd, a.rows, a.D);
     return cudaGetLastError();
-}
-
-template <typename TS, typename TB>
-cudaError_t fwd_sized(const void *x, const void *r, const float *weight, const float *scale, const Dropout &dp,
-                      float eps, void *h, void *y, float *rstd, int rows, int D, cudaStream_t st) {
-    if (D % 8 == 0) {
-        if (D <= 8192) return fwd_typed<TS, TB, true, 1>(x, r, weight, scale, dp, eps, h, y, rstd, rows, D, st);
-        return fwd_typed<TS, TB, true, 2>(x, r, weight, scale, dp, eps, h, y, rstd, rows, D, st);
-    }
-    if (D <= 4096) return fwd_typed<TS, TB, false, 1>(x, r, weight, scale, dp, eps, h, y, rstd, rows, D, st);
-    return fwd_typed<TS, TB, false, 4>(x, r, weight, scale, dp, eps, h, y, rstd, rows, D, st);
 }
 
 struct BwdArgs {
@@ -364,52 +572,77 @@ struct BwdArgs {
     const float *scale;
     Dropout dp;
     void *dx, *dr;
-    float *dweight, *dscale, *part;
-    int rows, D;
+    float *part;
+    int rows, D, grid;
 };
 
-template <typename TS, typename TB, bool AL, int VPT>
-cudaError_t bwd_typed(const BwdArgs &a, int grid, cudaStream_t st) {
-    float *part = grid == 1 && !a.dscale ? a.dweight : a.part;       // one CTA's sums are the result
-    const int threads = threads_for(a.D, AL, VPT);
-    auto kernel = threads <= 256   ? residual_norm_bwd_kernel<TS, TB, AL, VPT, 256>
-                  : threads <= 512 ? residual_norm_bwd_kernel<TS, TB, AL, VPT, 512>
-                                   : residual_norm_bwd_kernel<TS, TB, AL, VPT, 1024>;
-    kernel<<<grid, threads, 0, st>>>(
+template <typename TS, typename TB, bool AL, int VPT, int MAXT, bool RING>
+cudaError_t bwd_launch(const BwdArgs &a, int threads, cudaStream_t st) {
+    constexpr int bytes = VPT * vector_channels<TS, TB, AL>() * 2 * (int)(sizeof(TS) + sizeof(TB));
+    // Two rows in flight where that is at most 96 KB an SM, else one: more measured slower.
+    constexpr int S = RING ? (2 * bytes * (MAXT > 512 ? MAXT : 512) <= 98304 ? 2 : 1) : 0;
+    auto kernel = residual_norm_bwd_kernel<TS, TB, AL, VPT, MAXT, S>;
+    constexpr bool shared_channels = MAXT > 512 && S > 0;      // weight and scale, see Channels
+    const size_t smem = (size_t)MAXT * (bytes * S + (shared_channels ? 2 * 8 * 4 : 0));
+    const cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<a.grid, threads, smem, st>>>(
         static_cast<const TB *>(a.dy), static_cast<const TS *>(a.h), a.rstd, a.weight, static_cast<const TS *>(a.dh),
-        static_cast<const TB *>(a.dscale ? a.r : nullptr), a.scale, a.dp, static_cast<TS *>(a.dx),
-        static_cast<TB *>(a.dr), part, a.rows, a.D);
+        static_cast<const TB *>(a.r), a.scale, a.dp, static_cast<TS *>(a.dx), static_cast<TB *>(a.dr), a.part, a.rows,
+        a.D);
     return cudaGetLastError();
 }
 
-template <typename TS, typename TB> cudaError_t bwd_sized(const BwdArgs &a, int grid, cudaStream_t st) {
-    if (a.D % 8 == 0) return a.D <= 8192 ? bwd_typed<TS, TB, true, 1>(a, grid, st) : bwd_typed<TS, TB, true, 2>(a, grid, st);
-    return a.D <= 4096 ? bwd_typed<TS, TB, false, 1>(a, grid, st) : bwd_typed<TS, TB, false, 4>(a, grid, st);
+// The instance of LAUNCH (fwd_launch, bwd_launch) that a width needs; k vectors make 8 channels.
+#define GDN2_BY_WIDTH(LAUNCH)                                                                  \
+    constexpr int k = 8 / vector_channels<TS, TB, true>();                                     \
+    const Split s = split_for(a.D);                                                            \
+    if (s.aligned && !s.wide) {                                                                \
+        if (s.threads <= 64) return LAUNCH<TS, TB, true, k, 64, true>(a, s.threads, st);       \
+        if (s.threads <= 256) return LAUNCH<TS, TB, true, k, 256, true>(a, s.threads, st);     \
+        if (s.threads <= 512) return LAUNCH<TS, TB, true, k, 512, true>(a, s.threads, st);     \
+        return LAUNCH<TS, TB, true, k, 1024, true>(a, s.threads, st);                          \
+    }                                                                                          \
+    if (s.aligned) return LAUNCH<TS, TB, true, 2 * k, 1024, false>(a, s.threads, st);          \
+    if (s.wide) return LAUNCH<TS, TB, false, 4, 1024, false>(a, s.threads, st);                \
+    return LAUNCH<TS, TB, false, 1, 1024, false>(a, s.threads, st);
+
+template <typename TS, typename TB> cudaError_t fwd_sized(const FwdArgs &a, cudaStream_t st) {
+    GDN2_BY_WIDTH(fwd_launch)
 }
+template <typename TS, typename TB> cudaError_t bwd_sized(const BwdArgs &a, cudaStream_t st) {
+    GDN2_BY_WIDTH(bwd_launch)
+}
+#undef GDN2_BY_WIDTH
 
 // CTAs of the backward: the workspace holds one row of partial sums for each, so
-// the count goes by the sizes alone.
-int bwd_grid(int rows, int D) {
-    const int threads = threads_for(D, D % 8 == 0, D % 8 == 0 ? (D <= 8192 ? 1 : 2) : (D <= 4096 ? 1 : 4));
-    const int per_sm = threads >= 512 ? 1 : 512 / threads;
-    const long long cap = 148ll * (per_sm > 16 ? 16 : per_sm);
-    return (int)(rows < cap ? rows : cap);
-}
+// the count goes by the sizes alone (148 SMs).
+int bwd_grid(int rows, int D) { return grid_for(rows, split_for(D).threads, 512, 148); }
 
 }  // namespace
 
+// Launched while the grid that writes `part` still runs (programmatic dependent launch):
+// its CTAs wait for that grid's end before they read.
 cudaError_t launch_reduce_parts(const float *part, int G, int W, int D0, float *out0, float *out1, cudaStream_t st) {
-    reduce_parts_kernel<<<(W + 31) / 32, 1024, 0, st>>>(part, G, W, D0, out0, out1);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((W + 31) / 32);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, reduce_parts_kernel, part, G, W, D0, out0, out1);
 }
 
 cudaError_t launch_residual_norm(const void *x, const void *r, const float *weight, const float *scale, double p,
                                  const unsigned long long *rng, float eps, void *h, void *y, float *rstd, int rows,
                                  int D, gdn2_dtype stream_dt, gdn2_dtype dt, cudaStream_t st) {
     const Dropout dp{p > 0.0 && r ? rng : nullptr, (uint32_t)(p * 4294967296.0), (float)(1.0 / (1.0 - p))};
-    if (stream_dt == GDN2_BF16) return fwd_sized<bf16, bf16>(x, r, weight, scale, dp, eps, h, y, rstd, rows, D, st);
-    if (dt == GDN2_BF16) return fwd_sized<float, bf16>(x, r, weight, scale, dp, eps, h, y, rstd, rows, D, st);
-    return fwd_sized<float, float>(x, r, weight, scale, dp, eps, h, y, rstd, rows, D, st);
+    const FwdArgs a{x, r, weight, scale, dp, eps, h, y, rstd, rows, D};
+    if (stream_dt == GDN2_BF16) return fwd_sized<bf16, bf16>(a, st);
+    return dt == GDN2_BF16 ? fwd_sized<float, bf16>(a, st) : fwd_sized<float, float>(a, st);
 }
 
 size_t residual_norm_bwd_workspace_bytes(int rows, int D) {
@@ -422,12 +655,13 @@ cudaError_t launch_residual_norm_bwd(const void *dy, const void *h, const float 
                                      float *workspace, int rows, int D, gdn2_dtype stream_dt, gdn2_dtype dt,
                                      cudaStream_t st) {
     const Dropout dp{p > 0.0 ? rng : nullptr, (uint32_t)(p * 4294967296.0), (float)(1.0 / (1.0 - p))};
-    const BwdArgs a{dy, h, rstd, weight, dh, r, scale, dp, dx, dr, dweight, dscale, workspace, rows, D};
     const int grid = bwd_grid(rows, D);
-    cudaError_t e = stream_dt == GDN2_BF16 ? bwd_sized<bf16, bf16>(a, grid, st)
-                    : dt == GDN2_BF16      ? bwd_sized<float, bf16>(a, grid, st)
-                                           : bwd_sized<float, float>(a, grid, st);
-    if (e != cudaSuccess || (grid == 1 && !dscale)) return e;
+    const bool direct = grid == 1 && !dscale;          // one CTA's sums are the result
+    const BwdArgs a{dy, h, rstd, weight, dh, dscale ? r : nullptr, scale, dp, dx, dr, direct ? dweight : workspace, rows, D, grid};
+    const cudaError_t e = stream_dt == GDN2_BF16 ? bwd_sized<bf16, bf16>(a, st)
+                          : dt == GDN2_BF16      ? bwd_sized<float, bf16>(a, st)
+                                                 : bwd_sized<float, float>(a, st);
+    if (e != cudaSuccess || direct) return e;
     return launch_reduce_parts(workspace, grid, dscale ? 2 * D : D, D, dweight, dscale, st);
 }
 

@@ -10,6 +10,10 @@
 // dweight adds up in registers over the rows of a lane, then over the CTA in shared
 // memory; each CTA writes one row of partial sums, and a second launch adds those in
 // a fixed order, so the result does not change from call to call.
+//
+// Measured on a B200, 4 x 4,096 tokens x 16 heads of 128, BF16: 57.5 us = 5.83 TB/s (90 %
+// of a copy's rate) with three CTAs an SM; 71 us with four (the same kernel, more loads
+// in flight), 68 us with one row group at a time and five.
 #include "common.cuh"
 
 namespace gdn2 {
@@ -18,7 +22,8 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr int kThreads = 256;
 constexpr int kUnroll = 2;
-constexpr int kMaxGrid = 148 * 4;
+constexpr int kPerSm = 3;
+constexpr int kMaxGrid = 148 * kPerSm;
 
 template <typename T> struct Lane;
 template <> struct Lane<bf16> {
@@ -53,13 +58,14 @@ template <> struct Lane<float> {
 };
 
 template <typename T, int DV>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kPerSm)
 output_gate_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ o, const T *__restrict__ g,
                        const float *__restrict__ weight, float eps, T *__restrict__ d_o, T *__restrict__ d_g,
                        float *__restrict__ part, long long rows) {
     using L = Lane<T>;
     constexpr int N = L::N, LPR = DV / N, RPW = 32 / LPR, WARPS = kThreads / 32;
     __shared__ float acc[WARPS][DV];
+    cudaTriggerProgrammaticLaunchCompletion();       // the sums' launch may be set up; it waits for this grid's end
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR, at = lane % LPR;
     const long long groups = (rows + RPW - 1) / RPW, step = (long long)gridDim.x * WARPS * kUnroll;
     float wt[N], aw[N];

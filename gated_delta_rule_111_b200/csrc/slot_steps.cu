@@ -21,6 +21,7 @@
 // Token vectors are staged in shared memory eight tokens at a time, one warp per
 // token.
 #include "common.cuh"
+#include "f32x2.cuh"
 
 namespace gdn2 {
 namespace {
@@ -29,26 +30,6 @@ using bf16 = __nv_bfloat16;
 constexpr int kTile = 8;                  // tokens staged at a time
 
 __device__ unsigned int g_slot_conflict = 0;   // nonzero: a slot was named by two sequences, one of them writing it
-
-struct Pair { unsigned long long v; };
-__device__ __forceinline__ Pair pack2(float a, float b) {
-    Pair p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(a), "f"(b));
-    return p;
-}
-__device__ __forceinline__ void unpack2(Pair p, float &a, float &b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-    Pair d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-    return d;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-    Pair d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return d;
-}
 
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 __device__ __forceinline__ float warp_sum(float x) {
