@@ -150,7 +150,7 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 _current = contextlib.nullcontext()
@@ -162,6 +162,8 @@ def _on(device):
 
 
 def _need(t, name, dtype, shape, device):
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
@@ -172,10 +174,14 @@ def _need(t, name, dtype, shape, device):
         raise ValueError(f"{name}: must be contiguous")
 
 
+# The current stream's handle without a Stream object around it (2 us less a call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device):
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
 
 
 def gdn2_device_error(clear: bool = True) -> int:
@@ -449,19 +455,19 @@ def _rows(shape) -> int:
     return rows
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor from the pool of the stream the call runs on, so that the memory of a workspace freed
-    after the call is reused behind the call's kernels and not beside them."""
+def _empty(shape, dtype, like, stream):
+    """A new tensor on ``like``'s device from the pool of the stream the call runs on, so that the memory of a
+    workspace freed after the call is reused behind the call's kernels and not beside them."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _workspace(workspace, need, device, stream):
+def _workspace(workspace, need, like, stream):
     if workspace is None:
-        return _empty((max(need, 16),), torch.uint8, device, stream)
-    if workspace.device != device or not workspace.is_contiguous():
+        return _empty((max(need, 16),), torch.uint8, like, stream)
+    if workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor on the inputs' device")
     return workspace
 
@@ -503,15 +509,15 @@ def gdn2_residual_norm(x, r, weight, eps=1e-6, *, scale=None, p=0.0, rng=None, h
         if h is not None:
             raise ValueError("h: there is no addition to write without r")
     elif h is None:
-        h = _empty(shape, sdt, dev, stream)
+        h = _empty(shape, sdt, x, stream)
     else:
         _need(h, "h", sdt, shape, dev)
     if y is None:
-        y = _empty(shape, dt, dev, stream)
+        y = _empty(shape, dt, x, stream)
     else:
         _need(y, "y", dt, shape, dev)
     if rstd is None:
-        rstd = _empty(shape[:2], torch.float32, dev, stream)
+        rstd = _empty(shape[:2], torch.float32, x, stream)
     else:
         _need(rstd, "rstd", torch.float32, shape[:2], dev)
     with _on(dev):
@@ -561,10 +567,10 @@ def gdn2_residual_norm_bwd(dy, h, rstd, weight, *, dh=None, r=None, scale=None, 
         if t is not None:
             _need(t, name, d, s, dev)
         elif want:
-            t = _empty(s, d, dev, stream)
+            t = _empty(s, d, dy, stream)
         g[name] = t
     with _on(dev):
-        ws = _workspace(workspace, int(lib.gdn2_residual_norm_bwd_workspace_size(rows, D)), dev, stream)
+        ws = _workspace(workspace, int(lib.gdn2_residual_norm_bwd_workspace_size(rows, D)), dy, stream)
         _check(lib.gdn2_residual_norm_bwd(_ptr(dy), _ptr(h), _ptr(rstd), _ptr(weight), _ptr(dh),
                                           _ptr(r) if scale is not None else None, _ptr(scale), p, _ptr(rng),
                                           _ptr(g["dx"]), _ptr(g["dr"]), _ptr(g["dweight"]), _ptr(g["dscale"]),
@@ -597,12 +603,12 @@ def gdn2_output_gate_bwd(dy, o, g, weight, eps=1e-6, *, workspace=None, out=None
     for name, s, d in (("do", shape, dt), ("dg", shape, dt), ("dweight", (dv,), torch.float32)):
         t = out.get(name)
         if t is None:
-            t = _empty(s, d, dev, stream)
+            t = _empty(s, d, dy, stream)
         else:
             _need(t, name, d, s, dev)
         grads[name] = t
     with _on(dev):
-        ws = _workspace(workspace, int(lib.gdn2_output_gate_bwd_workspace_size(dv)), dev, stream)
+        ws = _workspace(workspace, int(lib.gdn2_output_gate_bwd_workspace_size(dv)), dy, stream)
         _check(lib.gdn2_output_gate_bwd(_ptr(dy), _ptr(o), _ptr(g), _ptr(weight), float(eps), _ptr(grads["do"]),
                                         _ptr(grads["dg"]), _ptr(grads["dweight"]), _ptr(ws),
                                         ws.numel() * ws.element_size(), B, T, H, dv, code, _stream(stream, dev)))
@@ -641,7 +647,7 @@ def _slot_steps(name, gates, q, k, v, alpha, b, w, pool, slots, cu_seqlens, keep
         _need(g, "g", dt, (T, H, dv), dev)
         _need(weight, "weight", torch.float32, (dv,), dev)
     if o is None:
-        o = _empty((T, H, dv), dt, dev, stream)
+        o = _empty((T, H, dv), dt, q, stream)
     else:
         _need(o, "o", dt, (T, H, dv), dev)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(b), _ptr(w), _ptr(pool), _ptr(slots), _ptr(cu_seqlens),

@@ -599,7 +599,7 @@ static gdn2_status slot_steps_common(const void *q, const void *k, const void *v
     if (gate && (!(eps >= 0.f) || eps > 3.0e38f))
         return fail(GDN2_ERR_INVALID_ARG, "%s", "eps must be finite and >= 0");
     if (N == 0 || H == 0 || T_total == 0) return GDN2_OK;
-    if ((long long)N * H > 0x7fffffffll) return fail(GDN2_ERR_UNSUPPORTED, "%s", "N * H must be below 2^31");
+    if ((long long)N * H >= 1ll << 30) return fail(GDN2_ERR_UNSUPPORTED, "%s", "N * H must be below 2^30");
     const size_t es = dt == GDN2_BF16 ? 2 : 4, gs = logits ? 2 : 4, tok = (size_t)T_total * H;
     const Buf ins[] = {{q, tok * d_k * es, "q"},
                        {k, tok * d_k * es, "k"},

@@ -11,15 +11,29 @@
 // registers and written once, whatever the number of tokens; a token costs 4 d_k d_v
 // fused multiply-adds in between.
 //
-// One CTA per (sequence, head); the columns of a state evolve independently, so a
-// warp owns 16 of them with all rows: lane = (row group of 8, column quad of 4), a
-// lane holds d_k / 8 rows x 4 columns, and a 16-byte load takes 64 contiguous bytes
-// of each of eight rows.  A token then needs no barrier: its two column sums
-// (Sbar^T (b k) and Sbar^T q) are added over the eight row groups by seven shuffles
-// that halve the number of sums at each step.  Rows are paired in 64-bit registers
-// for the packed FP32 multiply-adds of sm_100, which halves their issue slots.
-// Token vectors are staged in shared memory eight tokens at a time, one warp per
-// token.
+// Work: an item is one (sequence, head), a unit up to four tokens of it.  A CTA takes
+// items a grid apart and works through their units as a pipeline, with one barrier a
+// unit, so that no latency but the state's arrival is left between two of them:
+//   A  the unit's state, copied to shared memory asynchronously while the item before
+//      ran, goes to registers, and the next item's copies start;
+//   B  the unit's tokens, one after the other (below); the state after the last kept
+//      token is stored;
+//   C  the next unit's tokens are prepared (activations, norms, gates, products) by four
+//      warps, one token each, from copies that started two units ago;
+//   D  barrier;  E  the unit's outputs go through the epilogue, by the other warps.
+// One thread plans three units ahead; what it needs of a sequence comes by asynchronous
+// copies as well.
+//
+// Mapping: the columns of a state evolve independently, so a warp owns 16 of them with
+// all rows: lane = (row group of 8, column quad of 4), a lane holds d_k / 8 rows x 4
+// columns, and a 16-byte access takes 64 contiguous bytes of each of eight rows.  A
+// token then needs no barrier: its two column sums (Sbar^T (b k) and Sbar^T q) are added
+// over the eight row groups by seven shuffles that halve the number of sums at each step.
+// Rows are paired in 64-bit registers for the packed FP32 multiply-adds of sm_100, which
+// halves their issue slots.
+#include <type_traits>
+
+#include "async_copy.cuh"
 #include "common.cuh"
 #include "f32x2.cuh"
 
@@ -27,7 +41,9 @@ namespace gdn2 {
 namespace {
 
 using bf16 = __nv_bfloat16;
-constexpr int kTile = 8;                  // tokens staged at a time
+constexpr int kTile = 4;                  // tokens of a unit
+constexpr int kPlan = 8;                  // units in the plan's ring
+constexpr int kNear = 1;                  // slots of other sequences that a thread keeps in registers
 
 __device__ unsigned int g_slot_conflict = 0;   // nonzero: a slot was named by two sequences, one of them writing it
 
@@ -38,23 +54,23 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// N (2 or 4) consecutive channels of a token's vector
+// N (2 or 4) consecutive channels of a token's vector, from shared memory
 template <int N> __device__ __forceinline__ void load_n(const float *p, float (&v)[N]) {
     if (N == 4) {
-        const float4 r = __ldg(reinterpret_cast<const float4 *>(p));
+        const float4 r = *reinterpret_cast<const float4 *>(p);
         v[0] = r.x; v[1] = r.y; v[N - 2] = r.z; v[N - 1] = r.w;
     } else {
-        const float2 r = __ldg(reinterpret_cast<const float2 *>(p));
+        const float2 r = *reinterpret_cast<const float2 *>(p);
         v[0] = r.x; v[1] = r.y;
     }
 }
 template <int N> __device__ __forceinline__ void load_n(const bf16 *p, float (&v)[N]) {
     if (N == 4) {
-        const uint2 r = __ldg(reinterpret_cast<const uint2 *>(p));
+        const uint2 r = *reinterpret_cast<const uint2 *>(p);
         v[0] = __uint_as_float(r.x << 16); v[1] = __uint_as_float(r.x & 0xFFFF0000u);
         v[N - 2] = __uint_as_float(r.y << 16); v[N - 1] = __uint_as_float(r.y & 0xFFFF0000u);
     } else {
-        const uint32_t r = __ldg(reinterpret_cast<const uint32_t *>(p));
+        const uint32_t r = *reinterpret_cast<const uint32_t *>(p);
         v[0] = __uint_as_float(r << 16); v[1] = __uint_as_float(r & 0xFFFF0000u);
     }
 }
@@ -80,216 +96,388 @@ struct StepArgs {
     int N, T, H, n_slots;
 };
 
-template <typename TIn, int DK, int DV, bool LOGITS>
-__global__ void __launch_bounds__(DV * 2, DV == 128 ? 2 : 4)
-slot_steps_kernel(const StepArgs a) {
-    using TG = typename std::conditional<LOGITS, bf16, float>::type;
-    constexpr int WARPS = DV / 16, PAIRS = DK / 16, CK = DK / 32, CV = DV / 32;
-    __shared__ float4 s_ae[kTile][DK / 2], s_qk[kTile][DK / 2];       // (alpha, alpha', e, e'), (q, q', k, k') per row pair
-    __shared__ __align__(16) float s_z[kTile][DV], s_o[kTile][DV];
-    __shared__ float s_kq[kTile];
+// A sequence's entries as they stand in memory, and what they mean.
+struct Entry { int slot, t0, t1, keep; };
 
-    const int seq = blockIdx.x / a.H, head = blockIdx.x - seq * a.H;
+// A unit: tokens [row, row + count) of sequence `seq`, head `head`; `keep`: how many of them,
+// and of those after them, the stored state takes in; count 0: no more units.
+struct __align__(16) Unit { int row, count, head, slot, keep, first, seq, unused; };
+
+// The planning thread's own words in shared memory.
+struct Plan { int seq, head, t1, slot, keep, base, next_seq, next_head; Entry entry; };
+
+template <typename TIn, int DK, int DV, bool LOGITS> struct Shape {
+    using TG = typename std::conditional<LOGITS, bf16, float>::type;
+    static constexpr int THREADS = DV * 2, WARPS = THREADS / 32, PAIRS = DK / 16, CK = DK / 32, CV = DV / 32;
+    static_assert(WARPS >= kTile, "a warp for each token of a unit");
+    // a lane's bytes of one token, as they come: q, k, alpha, b, v, w
+    static constexpr int BK = CK * (int)sizeof(TIn), GK = CK * (int)sizeof(TG), BV = CV * (int)sizeof(TIn),
+                         GV = CV * (int)sizeof(TG), RAW = 2 * BK + 2 * GK + BV + GV;
+    // shared memory; what units share comes twice, by the unit's parity
+    static constexpr int VEC = kTile * DK * 8, ROW = kTile * DV * 4, GATES = kTile * 32 * BV;
+    static constexpr int STATE = 0, AE = STATE + DK * DV * 4, QK = AE + 2 * VEC, Z = QK + 2 * VEC, O = Z + 2 * ROW,
+                         GATE = O + 2 * ROW, RAWS = GATE + 2 * GATES, KQ = RAWS + kTile * 32 * RAW,
+                         UNITS = KQ + 2 * kTile * 4, PLAN = UNITS + kPlan * (int)sizeof(Unit),
+                         BYTES = PLAN + (int)sizeof(Plan);
+    static constexpr int CTAS = DV == 128 ? 2 : DK == 128 ? 3 : 4;      // an SM holds, by registers and shared memory
+};
+
+__device__ __forceinline__ Entry clamped(const StepArgs &a, int seq, Entry e) {
+    if (a.cu) {
+        e.t0 = min(max(e.t0, 0), a.T);
+        e.t1 = min(max(e.t1, e.t0), a.T);
+    } else {
+        e.t0 = seq;
+        e.t1 = seq + 1;
+    }
+    e.keep = a.keep ? min(max(e.keep, 0), e.t1 - e.t0) : e.t1 - e.t0;
+    return e;
+}
+__device__ __forceinline__ Entry load_entry(const StepArgs &a, int seq) {
+    Entry e{__ldg(a.slots + seq), 0, 0, 0};
+    if (a.cu) {
+        e.t0 = __ldg(a.cu + seq);
+        e.t1 = __ldg(a.cu + seq + 1);
+    }
+    if (a.keep) e.keep = __ldg(a.keep + seq);
+    return clamped(a, seq, e);
+}
+
+// The next unit of this CTA, by one thread.  `here`: the next item's entry has arrived in
+// plan.entry; otherwise, and where items without tokens are passed over, it is loaded.
+__device__ __forceinline__ void plan_unit(const StepArgs &a, Plan &p, Unit &u, bool here) {
+    bool first = false;
+    if (p.base + kTile < p.t1) {
+        p.base += kTile;
+        p.keep -= kTile;
+    } else {
+        Entry e{-1, 0, 0, 0};
+        while (p.next_seq < a.N) {
+            e = here ? clamped(a, p.next_seq, p.entry) : load_entry(a, p.next_seq);
+            here = false;
+            p.seq = p.next_seq;
+            p.head = p.next_head;
+            p.next_head += gridDim.x % a.H;
+            p.next_seq += gridDim.x / a.H;
+            if (p.next_head >= a.H) {
+                p.next_head -= a.H;
+                ++p.next_seq;
+            }
+            if (e.t0 < e.t1) break;
+        }
+        p.base = e.t0;
+        p.t1 = e.t1;
+        p.slot = e.slot;
+        p.keep = e.keep;
+        first = true;
+        if (p.next_seq < a.N) {                // for a later unit
+            copy_async<4>(smem_address(&p.entry.slot), a.slots + p.next_seq);
+            if (a.cu) {
+                copy_async<4>(smem_address(&p.entry.t0), a.cu + p.next_seq);
+                copy_async<4>(smem_address(&p.entry.t1), a.cu + p.next_seq + 1);
+            }
+            if (a.keep) copy_async<4>(smem_address(&p.entry.keep), a.keep + p.next_seq);
+        }
+    }
+    u = Unit{p.base, min(kTile, p.t1 - p.base), p.head, p.slot, p.keep, first, p.seq, 0};
+}
+
+template <typename TIn, int DK, int DV, bool LOGITS>
+__global__ void __launch_bounds__(DV * 2, Shape<TIn, DK, DV, LOGITS>::CTAS)
+slot_steps_kernel(const __grid_constant__ StepArgs a) {
+    using X = Shape<TIn, DK, DV, LOGITS>;
+    using TG = typename X::TG;
+    constexpr int THREADS = X::THREADS, WARPS = X::WARPS, PAIRS = X::PAIRS, CK = X::CK, CV = X::CV;
+    extern __shared__ __align__(16) unsigned char sm[];
+    Unit *units = reinterpret_cast<Unit *>(sm + X::UNITS);
+    Plan &plan = *reinterpret_cast<Plan *>(sm + X::PLAN);
+
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rg = lane >> 2, col = warp * 16 + (lane & 3) * 4;
+    const int late = (warp + WARPS / 2) % WARPS;           // the token whose output this warp finishes
+    const bool planner = tid == THREADS - 1;
+    const uint32_t state_at = smem_address(sm + X::STATE) + tid * 16;
 
-    int t0 = seq, t1 = seq + 1;
-    if (a.cu) {
-        t0 = min(max(__ldg(a.cu + seq), 0), a.T);
-        t1 = min(max(__ldg(a.cu + seq + 1), t0), a.T);
-    }
-    if (t0 >= t1) return;
-    const int slot = __ldg(a.slots + seq);
-    int keep = t1 - t0;
-    if (a.keep) keep = min(max(__ldg(a.keep + seq), 0), keep);
-    bool refused = slot < 0 || slot >= a.n_slots;
-
-    // the state: rows 2m and 2m + 1 for m = rg + 8 j, four columns each
-    float *Sh = a.pool + ((size_t)(refused ? 0 : slot) * a.H + head) * (DK * DV);
-    Pair S[PAIRS][4];
-    if (!refused) {
-        float4 r0[PAIRS], r1[PAIRS];
+    // Asynchronous copies of what this thread itself reads later: its part of a state, its
+    // lane's channels of the token that its warp prepares and of the gate that it applies.
+    auto fetch_state = [&](const Unit &u) {
+        if (!u.first || u.count <= 0 || u.slot < 0 || u.slot >= a.n_slots) return;
+        const float *p = a.pool + ((size_t)u.slot * a.H + u.head) * (DK * DV) + (size_t)(2 * rg) * DV + col;
 #pragma unroll
         for (int j = 0; j < PAIRS; ++j) {
-            const float *p = Sh + (size_t)(2 * (rg + 8 * j)) * DV + col;
-            r0[j] = __ldcs(reinterpret_cast<const float4 *>(p));
-            r1[j] = __ldcs(reinterpret_cast<const float4 *>(p + DV));
+            copy_async<16>(state_at + (2 * j) * THREADS * 16, p + 16 * j * DV);
+            copy_async<16>(state_at + (2 * j + 1) * THREADS * 16, p + (16 * j + 1) * DV);
         }
+    };
+    auto fetch_token = [&](const Unit &u) {
+        if (warp >= u.count) return;
+        const size_t row = (size_t)(u.row + warp) * a.H + u.head, ok = row * DK + lane * CK, ov = row * DV + lane * CV;
+        uint32_t at = smem_address(sm + X::RAWS) + warp * 32 * X::RAW;
+        copy_async<X::BK>(at + lane * X::BK, static_cast<const TIn *>(a.q) + ok);
+        copy_async<X::BK>((at += 32 * X::BK) + lane * X::BK, static_cast<const TIn *>(a.k) + ok);
+        copy_async<X::GK>((at += 32 * X::BK) + lane * X::GK, static_cast<const TG *>(a.alpha) + ok);
+        copy_async<X::GK>((at += 32 * X::GK) + lane * X::GK, static_cast<const TG *>(a.b) + ok);
+        copy_async<X::BV>((at += 32 * X::GK) + lane * X::BV, static_cast<const TIn *>(a.v) + ov);
+        copy_async<X::GV>((at += 32 * X::BV) + lane * X::GV, static_cast<const TG *>(a.w) + ov);
+    };
+    auto fetch_gate = [&](const Unit &u, int parity) {
+        if (!a.gate || late >= u.count) return;
+        copy_async<X::BV>(smem_address(sm + X::GATE) + parity * X::GATES + (late * 32 + lane) * X::BV,
+                          static_cast<const TIn *>(a.gate) + ((size_t)(u.row + late) * a.H + u.head) * DV + lane * CV);
+    };
+    // The token that this warp prepares, from its copies to the vectors that B reads.
+    auto prepare = [&](const Unit &u, int parity) {
+        if (warp >= u.count) return;
+        const unsigned char *raw = sm + X::RAWS + warp * 32 * X::RAW;
+        float q[CK], k[CK], al[CK], b[CK], v[CV], w[CV];
+        load_n<CK>(reinterpret_cast<const TIn *>(raw + lane * X::BK), q);
+        load_n<CK>(reinterpret_cast<const TIn *>((raw += 32 * X::BK) + lane * X::BK), k);
+        load_n<CK>(reinterpret_cast<const TG *>((raw += 32 * X::BK) + lane * X::GK), al);
+        load_n<CK>(reinterpret_cast<const TG *>((raw += 32 * X::GK) + lane * X::GK), b);
+        load_n<CV>(reinterpret_cast<const TIn *>((raw += 32 * X::GK) + lane * X::BV), v);
+        load_n<CV>(reinterpret_cast<const TG *>((raw += 32 * X::BV) + lane * X::GV), w);
+        if (LOGITS) {
+            float sq = 0.f, sk = 0.f;
 #pragma unroll
-        for (int j = 0; j < PAIRS; ++j) {
-            S[j][0] = pack2(r0[j].x, r1[j].x); S[j][1] = pack2(r0[j].y, r1[j].y);
-            S[j][2] = pack2(r0[j].z, r1[j].z); S[j][3] = pack2(r0[j].w, r1[j].w);
+            for (int e = 0; e < CK; ++e) {
+                q[e] *= sigmoid(q[e]);
+                k[e] *= sigmoid(k[e]);
+                sq = fmaf(q[e], q[e], sq);
+                sk = fmaf(k[e], k[e], sk);
+                al[e] = sigmoid(-al[e]);
+                b[e] = sigmoid(b[e]);
+            }
+            sq = warp_sum(sq);
+            sk = warp_sum(sk);
+            const float iq = sq > 0.f ? rsqrtf(sq) : 0.f, ik = sk > 0.f ? rsqrtf(sk) : 0.f;   // a zero row stays zero
+#pragma unroll
+            for (int e = 0; e < CK; ++e) {
+                q[e] *= iq;
+                k[e] *= ik;
+            }
+#pragma unroll
+            for (int e = 0; e < CV; ++e) {
+                v[e] *= sigmoid(v[e]);
+                w[e] = sigmoid(w[e]);
+            }
         }
-    }
-
+        float kq = 0.f;
+#pragma unroll
+        for (int e = 0; e < CK; ++e) kq = fmaf(k[e], q[e], kq);
+        kq = warp_sum(kq);
+        if (lane == 0) reinterpret_cast<float *>(sm + X::KQ)[parity * kTile + warp] = kq;
+        // per row pair: (alpha, alpha', e, e') and (q, q', k, k')
+        float4 *ae = reinterpret_cast<float4 *>(sm + X::AE + parity * X::VEC) + warp * (DK / 2);
+        float4 *qk = reinterpret_cast<float4 *>(sm + X::QK + parity * X::VEC) + warp * (DK / 2);
+#pragma unroll
+        for (int e = 0; e < CK; e += 2) {
+            ae[(lane * CK + e) / 2] = make_float4(al[e], al[e + 1], b[e] * k[e], b[e + 1] * k[e + 1]);
+            qk[(lane * CK + e) / 2] = make_float4(q[e], q[e + 1], k[e], k[e + 1]);
+        }
+        float *z = reinterpret_cast<float *>(sm + X::Z + parity * X::ROW) + warp * DV;
+#pragma unroll
+        for (int e = 0; e < CV; ++e) z[lane * CV + e] = w[e] * v[e];
+    };
     // Two sequences that name one slot would race if either writes it: both are refused.
-    bool clash = false;
-    for (int m = tid; m < a.N; m += DV * 2) {
-        if (m == seq || refused || __ldg(a.slots + m) != slot) continue;
-        int len = 1;
-        if (a.cu) {
-            const int u0 = min(max(__ldg(a.cu + m), 0), a.T);
-            len = min(max(__ldg(a.cu + m + 1), u0), a.T) - u0;
-        }
-        const int other = a.keep ? min(max(__ldg(a.keep + m), 0), len) : len;
-        clash |= len > 0 && (keep > 0 || other > 0);
+    int near[kNear];
+#pragma unroll
+    for (int i = 0; i < kNear; ++i) near[i] = tid + i * THREADS < a.N ? __ldg(a.slots + tid + i * THREADS) : -1;
+    auto clashes = [&](const Unit &u) {
+        if (!u.first || u.count <= 0 || u.slot < 0 || u.slot >= a.n_slots) return false;
+        bool clash = false;
+        auto compare = [&](int m, int slot) {
+            if (slot != u.slot || m == u.seq) return;
+            const Entry other = load_entry(a, m);
+            clash |= other.t0 < other.t1 && (u.keep > 0 || other.keep > 0);
+        };
+#pragma unroll
+        for (int i = 0; i < kNear; ++i) compare(tid + i * THREADS, near[i]);
+        for (int m = tid + kNear * THREADS; m < a.N; m += THREADS) compare(m, __ldg(a.slots + m));
+        return clash;
+    };
+
+    if (planner) {
+        plan = Plan{0, 0, 0, 0, 0, 0, (int)blockIdx.x / a.H, (int)blockIdx.x % a.H, {}};
+        plan_unit(a, plan, units[0], false);
+        copy_commit();
+        copy_wait<0>();
+        plan_unit(a, plan, units[1], true);
+        copy_commit();
+        copy_wait<0>();
+        plan_unit(a, plan, units[2], true);
+    }
+    __syncthreads();
+    bool dead;                                 // the item has no state: its outputs are zero
+    {
+        const Unit u = units[0];
+        fetch_token(u);
+        fetch_gate(u, 0);
+        copy_commit();
+        fetch_state(u);
+        copy_commit();
+        const bool clash = clashes(u);
+        copy_wait<1>();
+        prepare(u, 0);
+        fetch_token(units[1]);
+        copy_commit();
+        dead = __syncthreads_or(clash);
+        if (dead && planner) atomicOr(&g_slot_conflict, 1u);
     }
 
-    for (int base = t0; base < t1; base += kTile) {
-        const int count = min(kTile, t1 - base);
-        for (int i = warp; i < count; i += WARPS) {
-            const size_t row = (size_t)(base + i) * a.H + head, ok = row * DK + lane * CK, ov = row * DV + lane * CV;
-            float q[CK], k[CK], al[CK], b[CK], v[CV], w[CV];
-            load_n<CK>(static_cast<const TIn *>(a.q) + ok, q);
-            load_n<CK>(static_cast<const TIn *>(a.k) + ok, k);
-            load_n<CK>(static_cast<const TG *>(a.alpha) + ok, al);
-            load_n<CK>(static_cast<const TG *>(a.b) + ok, b);
-            load_n<CV>(static_cast<const TIn *>(a.v) + ov, v);
-            load_n<CV>(static_cast<const TG *>(a.w) + ov, w);
-            if (LOGITS) {
-                float sq = 0.f, sk = 0.f;
-#pragma unroll
-                for (int e = 0; e < CK; ++e) {
-                    q[e] *= sigmoid(q[e]);
-                    k[e] *= sigmoid(k[e]);
-                    sq = fmaf(q[e], q[e], sq);
-                    sk = fmaf(k[e], k[e], sk);
-                    al[e] = sigmoid(-al[e]);
-                    b[e] = sigmoid(b[e]);
-                }
-                sq = warp_sum(sq);
-                sk = warp_sum(sk);
-                const float iq = sq > 0.f ? rsqrtf(sq) : 0.f, ik = sk > 0.f ? rsqrtf(sk) : 0.f;   // a zero row stays zero
-#pragma unroll
-                for (int e = 0; e < CK; ++e) {
-                    q[e] *= iq;
-                    k[e] *= ik;
-                }
-#pragma unroll
-                for (int e = 0; e < CV; ++e) {
-                    v[e] *= sigmoid(v[e]);
-                    w[e] = sigmoid(w[e]);
-                }
-            }
-            float kq = 0.f;
-#pragma unroll
-            for (int e = 0; e < CK; ++e) kq = fmaf(k[e], q[e], kq);
-            kq = warp_sum(kq);
-            if (lane == 0) s_kq[i] = kq;
-#pragma unroll
-            for (int e = 0; e < CK; e += 2) {
-                s_ae[i][(lane * CK + e) / 2] = make_float4(al[e], al[e + 1], b[e] * k[e], b[e + 1] * k[e + 1]);
-                s_qk[i][(lane * CK + e) / 2] = make_float4(q[e], q[e + 1], k[e], k[e + 1]);
-            }
-#pragma unroll
-            for (int e = 0; e < CV; ++e) s_z[i][lane * CV + e] = w[e] * v[e];
-        }
-        if (base == t0) {
-            if (__syncthreads_or(clash)) {
-                if (tid == 0) atomicOr(&g_slot_conflict, 1u);
-                refused = true;
-            }
-        } else {
-            __syncthreads();
-        }
-        if (refused) {                     // no state: this sequence's outputs are zero
-            for (int i = tid; i < (t1 - t0) * DV; i += DV * 2)
-                Elem<TIn>::store(static_cast<TIn *>(a.o) + ((size_t)(t0 + i / DV) * a.H + head) * DV + i % DV, 0.f);
-            return;
-        }
+    Pair S[PAIRS][4];                          // rows 2m and 2m + 1 for m = rg + 8 j, four columns each
+    for (int n = 0;; ++n) {
+        const int parity = n & 1;
+        const int count = units[n % kPlan].count;
+        if (count <= 0) break;
 
-        for (int i = 0; i < count; ++i) {
-            Pair r[4], p[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) r[c].v = p[c].v = 0ull;
-#pragma unroll
-            for (int j = 0; j < PAIRS; ++j) {
-                const float4 ae = s_ae[i][rg + 8 * j], qk = s_qk[i][rg + 8 * j];
-                const Pair al = pack2(ae.x, ae.y), e = pack2(ae.z, ae.w), q = pack2(qk.x, qk.y);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    S[j][c] = mul2(S[j][c], al);
-                    r[c] = fma2(S[j][c], e, r[c]);
-                    p[c] = fma2(S[j][c], q, p[c]);
-                }
-            }
-            // Add over the row groups: lane bit 4 keeps one of the two sums, bits 3 and 2 one column.
-            float x[4];
-            const bool up = lane & 16;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float r0, r1, p0, p1;
-                unpack2(r[c], r0, r1);
-                unpack2(p[c], p0, p1);
-                r0 += r1;
-                p0 += p1;
-                x[c] = (up ? p0 : r0) + __shfl_xor_sync(0xffffffffu, up ? r0 : p0, 16);
-            }
-            const bool b3 = lane & 8, b2 = lane & 4;
-            const float y0 = (b3 ? x[2] : x[0]) + __shfl_xor_sync(0xffffffffu, b3 ? x[0] : x[2], 8);
-            const float y1 = (b3 ? x[3] : x[1]) + __shfl_xor_sync(0xffffffffu, b3 ? x[1] : x[3], 8);
-            const float mine = (b2 ? y1 : y0) + __shfl_xor_sync(0xffffffffu, b2 ? y0 : y1, 4);
-            const float other = __shfl_xor_sync(0xffffffffu, mine, 16);
-            const int c_own = col + (b3 ? 2 : 0) + (b2 ? 1 : 0);
-            const float u = s_z[i][c_own] - (up ? other : mine);
-            if (up) s_o[i][c_own] = fmaf(s_kq[i], u, mine);
-            Pair u2[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float uc = __shfl_sync(0xffffffffu, u, (lane & 3) | (c & 1) << 2 | (c & 2) << 2);
-                u2[c] = pack2(uc, uc);
-            }
-#pragma unroll
-            for (int j = 0; j < PAIRS; ++j) {
-                const float4 qk = s_qk[i][rg + 8 * j];
-                const Pair k = pack2(qk.z, qk.w);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) S[j][c] = fma2(k, u2[c], S[j][c]);
-            }
-            if (base + i - t0 + 1 == keep) {
+        // A
+        copy_wait<1>();                        // all but the next unit's tokens
+        if (units[n % kPlan].first) {
+            const int slot = units[n % kPlan].slot;
+            dead |= slot < 0 || slot >= a.n_slots;
+            if (!dead) {
 #pragma unroll
                 for (int j = 0; j < PAIRS; ++j) {
-                    float4 r0, r1;
-                    unpack2(S[j][0], r0.x, r1.x); unpack2(S[j][1], r0.y, r1.y);
-                    unpack2(S[j][2], r0.z, r1.z); unpack2(S[j][3], r0.w, r1.w);
-                    float *p2 = Sh + (size_t)(2 * (rg + 8 * j)) * DV + col;
-                    __stcs(reinterpret_cast<float4 *>(p2), r0);
-                    __stcs(reinterpret_cast<float4 *>(p2 + DV), r1);
+                    uint4 x, y;
+                    load_shared(state_at + (2 * j) * THREADS * 16, x);
+                    load_shared(state_at + (2 * j + 1) * THREADS * 16, y);
+                    S[j][0] = pack2(__uint_as_float(x.x), __uint_as_float(y.x));
+                    S[j][1] = pack2(__uint_as_float(x.y), __uint_as_float(y.y));
+                    S[j][2] = pack2(__uint_as_float(x.z), __uint_as_float(y.z));
+                    S[j][3] = pack2(__uint_as_float(x.w), __uint_as_float(y.w));
                 }
             }
         }
-        __syncthreads();
-        for (int i = warp; i < count; i += WARPS) {
-            const size_t ov = ((size_t)(base + i) * a.H + head) * DV + lane * CV;
-            float x[CV];
+        if (planner) plan_unit(a, plan, units[(n + 3) % kPlan], true);
+        fetch_state(units[(n + 1) % kPlan]);
+        copy_commit();
+
+        // B
+        if (!dead) {
+            const float4 *s_ae = reinterpret_cast<const float4 *>(sm + X::AE + parity * X::VEC) + rg;
+            const float4 *s_qk = reinterpret_cast<const float4 *>(sm + X::QK + parity * X::VEC) + rg;
+            const float *s_z = reinterpret_cast<const float *>(sm + X::Z + parity * X::ROW);
+            const float *s_kq = reinterpret_cast<const float *>(sm + X::KQ) + parity * kTile;
+            float *s_o = reinterpret_cast<float *>(sm + X::O + parity * X::ROW);
+            const bool up = lane & 16, b3 = lane & 8, b2 = lane & 4;
+            const int c_own = col + (b3 ? 2 : 0) + (b2 ? 1 : 0);
+            const int last = units[n % kPlan].keep - 1;
+            for (int i = 0; i < count; ++i) {
+                Pair r[4], p[4];
 #pragma unroll
-            for (int e = 0; e < CV; ++e) x[e] = s_o[i][lane * CV + e];
+                for (int c = 0; c < 4; ++c) r[c].v = p[c].v = 0ull;
+#pragma unroll
+                for (int j = 0; j < PAIRS; ++j) {
+                    const float4 ae = s_ae[i * (DK / 2) + 8 * j], qk = s_qk[i * (DK / 2) + 8 * j];
+                    const Pair al = pack2(ae.x, ae.y), e = pack2(ae.z, ae.w), q = pack2(qk.x, qk.y);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        S[j][c] = mul2(S[j][c], al);
+                        r[c] = fma2(S[j][c], e, r[c]);
+                        p[c] = fma2(S[j][c], q, p[c]);
+                    }
+                }
+                // Add over the row groups: lane bit 4 keeps one of the two sums, bits 3 and 2 one column.
+                float x[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float r0, r1, p0, p1;
+                    unpack2(r[c], r0, r1);
+                    unpack2(p[c], p0, p1);
+                    r0 += r1;
+                    p0 += p1;
+                    x[c] = (up ? p0 : r0) + __shfl_xor_sync(0xffffffffu, up ? r0 : p0, 16);
+                }
+                const float y0 = (b3 ? x[2] : x[0]) + __shfl_xor_sync(0xffffffffu, b3 ? x[0] : x[2], 8);
+                const float y1 = (b3 ? x[3] : x[1]) + __shfl_xor_sync(0xffffffffu, b3 ? x[1] : x[3], 8);
+                const float mine = (b2 ? y1 : y0) + __shfl_xor_sync(0xffffffffu, b2 ? y0 : y1, 4);
+                const float other = __shfl_xor_sync(0xffffffffu, mine, 16);
+                const float u = s_z[i * DV + c_own] - (up ? other : mine);
+                if (up) s_o[i * DV + c_own] = fmaf(s_kq[i], u, mine);
+                Pair u2[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float uc = __shfl_sync(0xffffffffu, u, (lane & 3) | (c & 1) << 2 | (c & 2) << 2);
+                    u2[c] = pack2(uc, uc);
+                }
+#pragma unroll
+                for (int j = 0; j < PAIRS; ++j) {
+                    const float2 kk = reinterpret_cast<const float2 *>(s_qk + i * (DK / 2) + 8 * j)[1];
+                    const Pair k = pack2(kk.x, kk.y);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) S[j][c] = fma2(k, u2[c], S[j][c]);
+                }
+                if (i == last) {
+                    float *to = a.pool + ((size_t)units[n % kPlan].slot * a.H + units[n % kPlan].head) * (DK * DV) +
+                                (size_t)(2 * rg) * DV + col;
+#pragma unroll
+                    for (int j = 0; j < PAIRS; ++j) {
+                        float4 r0, r1;
+                        unpack2(S[j][0], r0.x, r1.x); unpack2(S[j][1], r0.y, r1.y);
+                        unpack2(S[j][2], r0.z, r1.z); unpack2(S[j][3], r0.w, r1.w);
+                        __stcs(reinterpret_cast<float4 *>(to + 16 * j * DV), r0);
+                        __stcs(reinterpret_cast<float4 *>(to + (16 * j + 1) * DV), r1);
+                    }
+                }
+            }
+        }
+
+        // C
+        copy_wait<1>();                        // all but the next item's state
+        prepare(units[(n + 1) % kPlan], parity ^ 1);
+        fetch_token(units[(n + 2) % kPlan]);
+        fetch_gate(units[(n + 1) % kPlan], parity ^ 1);
+        copy_commit();
+        const bool clash = clashes(units[(n + 1) % kPlan]);
+
+        // D
+        const bool next_dead = __syncthreads_or(clash);
+
+        // E
+        if (late < count) {
+            const Unit &u = units[n % kPlan];
+            const size_t ov = ((size_t)(u.row + late) * a.H + u.head) * DV + lane * CV;
+            float x[CV];
+            load_n<CV>(reinterpret_cast<const float *>(sm + X::O + parity * X::ROW) + late * DV + lane * CV, x);
             if (a.gate) {
                 float gv[CV], ss = 0.f;
-                load_n<CV>(static_cast<const TIn *>(a.gate) + ov, gv);
+                load_n<CV>(reinterpret_cast<const TIn *>(sm + X::GATE + parity * X::GATES + (late * 32 + lane) * X::BV), gv);
 #pragma unroll
                 for (int e = 0; e < CV; ++e) ss = fmaf(x[e], x[e], ss);
                 const float rs = rsqrtf(warp_sum(ss) * (1.f / DV) + a.eps);
 #pragma unroll
                 for (int e = 0; e < CV; ++e) x[e] = x[e] * rs * __ldg(a.weight + lane * CV + e) * sigmoid(gv[e]);
             }
+            if (dead) {
+#pragma unroll
+                for (int e = 0; e < CV; ++e) x[e] = 0.f;
+            }
             store_n<CV>(static_cast<TIn *>(a.o) + ov, x);
+        }
+        if (units[(n + 1) % kPlan].first) {
+            dead = next_dead;
+            if (dead && planner) atomicOr(&g_slot_conflict, 1u);
         }
     }
 }
 
-template <typename TIn, bool LOGITS>
-cudaError_t launch_dims(const StepArgs &a, int dk, int dv, cudaStream_t st) {
-    const unsigned grid = (unsigned)a.N * (unsigned)a.H;
-    if (dk == 128 && dv == 128)
-        slot_steps_kernel<TIn, 128, 128, LOGITS><<<grid, 256, 0, st>>>(a);
-    else if (dk == 64 && dv == 64)
-        slot_steps_kernel<TIn, 64, 64, LOGITS><<<grid, 128, 0, st>>>(a);
-    else if (dk == 128)
-        slot_steps_kernel<TIn, 128, 64, LOGITS><<<grid, 128, 0, st>>>(a);
-    else
-        slot_steps_kernel<TIn, 64, 128, LOGITS><<<grid, 256, 0, st>>>(a);
+template <typename TIn, int DK, int DV, bool LOGITS> cudaError_t launch_typed(const StepArgs &a, cudaStream_t st) {
+    using X = Shape<TIn, DK, DV, LOGITS>;
+    int dev = 0, sms = 148;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(slot_steps_kernel<TIn, DK, DV, LOGITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 X::BYTES);
+    if (e != cudaSuccess) return e;
+    const int items = a.N * a.H, cap = sms * X::CTAS;
+    slot_steps_kernel<TIn, DK, DV, LOGITS><<<items < cap ? items : cap, X::THREADS, X::BYTES, st>>>(a);
     return cudaGetLastError();
+}
+
+template <typename TIn, bool LOGITS> cudaError_t launch_dims(const StepArgs &a, int dk, int dv, cudaStream_t st) {
+    if (dk == 128) return dv == 128 ? launch_typed<TIn, 128, 128, LOGITS>(a, st) : launch_typed<TIn, 128, 64, LOGITS>(a, st);
+    return dv == 128 ? launch_typed<TIn, 64, 128, LOGITS>(a, st) : launch_typed<TIn, 64, 64, LOGITS>(a, st);
 }
 
 }  // namespace
