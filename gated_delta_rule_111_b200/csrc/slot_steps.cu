@@ -103,8 +103,11 @@ struct Entry { int slot, t0, t1, keep; };
 // and of those after them, the stored state takes in; count 0: no more units.
 struct __align__(16) Unit { int row, count, head, slot, keep, first, seq, unused; };
 
-// The planning thread's own words in shared memory.
-struct Plan { int seq, head, t1, slot, keep, base, next_seq, next_head; Entry entry; };
+// The planning thread's own words in shared memory: the item in hand; the next round of
+// items, its sequence (-1: there is none) and head; the entries of the first rounds, and
+// of a later one where it was `sent` for.
+constexpr int kEarly = 4;
+struct Plan { int seq, head, t1, slot, keep, base, round, next_seq, next_head, sent, unused[2]; Entry early[kEarly], entry; };
 
 template <typename TIn, int DK, int DV, bool LOGITS> struct Shape {
     using TG = typename std::conditional<LOGITS, bf16, float>::type;
@@ -118,7 +121,7 @@ template <typename TIn, int DK, int DV, bool LOGITS> struct Shape {
     static constexpr int STATE = 0, AE = STATE + DK * DV * 4, QK = AE + 2 * VEC, Z = QK + 2 * VEC, O = Z + 2 * ROW,
                          GATE = O + 2 * ROW, RAWS = GATE + 2 * GATES, KQ = RAWS + kTile * 32 * RAW,
                          UNITS = KQ + 2 * kTile * 4, PLAN = UNITS + kPlan * (int)sizeof(Unit),
-                         BYTES = PLAN + (int)sizeof(Plan);
+                         ORDER = PLAN + (int)sizeof(Plan), BYTES = ORDER + 2 * THREADS;
     static constexpr int CTAS = DV == 128 ? 2 : DK == 128 ? 3 : 4;      // an SM holds, by registers and shared memory
 };
 
@@ -143,26 +146,32 @@ __device__ __forceinline__ Entry load_entry(const StepArgs &a, int seq) {
     return clamped(a, seq, e);
 }
 
-// The next unit of this CTA, by one thread.  `here`: the next item's entry has arrived in
-// plan.entry; otherwise, and where items without tokens are passed over, it is loaded.
-__device__ __forceinline__ void plan_unit(const StepArgs &a, Plan &p, Unit &u, bool here) {
+// The sequence of this CTA's item of a round (-1: none) and its head.  Items are sequences x
+// heads, the sequences in the order of `order` where there is one; every other round then
+// goes through the CTAs backwards.
+__device__ __forceinline__ int item_of(const StepArgs &a, const unsigned short *order, int round, int &head) {
+    const int grid = gridDim.x, b = blockIdx.x;
+    const long long at = (long long)round * grid + (order && round & 1 ? grid - 1 - b : b);
+    if (at >= (long long)a.N * a.H) return -1;
+    const int seq = (int)at / a.H;
+    head = (int)at - seq * a.H;
+    return order ? order[seq] : seq;
+}
+
+// The next unit of this CTA, by one thread.  `ahead`: send for the entry after it.
+__device__ __forceinline__ void plan_unit(const StepArgs &a, const unsigned short *order, Plan &p, Unit &u, bool ahead) {
     bool first = false;
     if (p.base + kTile < p.t1) {
         p.base += kTile;
         p.keep -= kTile;
     } else {
         Entry e{-1, 0, 0, 0};
-        while (p.next_seq < a.N) {
-            e = here ? clamped(a, p.next_seq, p.entry) : load_entry(a, p.next_seq);
-            here = false;
+        while (p.next_seq >= 0) {              // past items without tokens
+            e = p.round < kEarly ? p.early[p.round] : p.sent ? clamped(a, p.next_seq, p.entry) : load_entry(a, p.next_seq);
             p.seq = p.next_seq;
             p.head = p.next_head;
-            p.next_head += gridDim.x % a.H;
-            p.next_seq += gridDim.x / a.H;
-            if (p.next_head >= a.H) {
-                p.next_head -= a.H;
-                ++p.next_seq;
-            }
+            p.sent = 0;
+            p.next_seq = item_of(a, order, ++p.round, p.next_head);
             if (e.t0 < e.t1) break;
         }
         p.base = e.t0;
@@ -170,14 +179,15 @@ __device__ __forceinline__ void plan_unit(const StepArgs &a, Plan &p, Unit &u, b
         p.slot = e.slot;
         p.keep = e.keep;
         first = true;
-        if (p.next_seq < a.N) {                // for a later unit
-            copy_async<4>(smem_address(&p.entry.slot), a.slots + p.next_seq);
-            if (a.cu) {
-                copy_async<4>(smem_address(&p.entry.t0), a.cu + p.next_seq);
-                copy_async<4>(smem_address(&p.entry.t1), a.cu + p.next_seq + 1);
-            }
-            if (a.keep) copy_async<4>(smem_address(&p.entry.keep), a.keep + p.next_seq);
+    }
+    if (ahead && !p.sent && p.next_seq >= 0 && p.round >= kEarly) {
+        copy_async<4>(smem_address(&p.entry.slot), a.slots + p.next_seq);
+        if (a.cu) {
+            copy_async<4>(smem_address(&p.entry.t0), a.cu + p.next_seq);
+            copy_async<4>(smem_address(&p.entry.t1), a.cu + p.next_seq + 1);
         }
+        if (a.keep) copy_async<4>(smem_address(&p.entry.keep), a.keep + p.next_seq);
+        p.sent = 1;
     }
     u = Unit{p.base, min(kTile, p.t1 - p.base), p.head, p.slot, p.keep, first, p.seq, 0};
 }
@@ -296,15 +306,38 @@ slot_steps_kernel(const __grid_constant__ StepArgs a) {
         return clash;
     };
 
-    if (planner) {
-        plan = Plan{0, 0, 0, 0, 0, 0, (int)blockIdx.x / a.H, (int)blockIdx.x % a.H, {}};
-        plan_unit(a, plan, units[0], false);
-        copy_commit();
-        copy_wait<0>();
-        plan_unit(a, plan, units[1], true);
-        copy_commit();
-        copy_wait<0>();
-        plan_unit(a, plan, units[2], true);
+    // Where sequences have different lengths and a CTA gets few of them, they are taken from the
+    // longest to the shortest, there and back, so that the CTAs' sums of tokens are alike.
+    const unsigned short *order = nullptr;
+    if (a.cu && a.N <= THREADS && a.N * a.H > (int)gridDim.x) {
+        unsigned short *by_length = reinterpret_cast<unsigned short *>(sm + X::ORDER);
+        int *lengths = reinterpret_cast<int *>(sm + X::AE);         // free until the first token is prepared
+        int mine = 0;
+        if (tid < a.N) {
+            const Entry e = load_entry(a, tid);
+            lengths[tid] = mine = e.t1 - e.t0;
+        }
+        __syncthreads();
+        if (tid < a.N) {
+            int rank = 0;
+            for (int m = 0; m < a.N; ++m) rank += lengths[m] > mine || (lengths[m] == mine && m < tid);
+            by_length[rank] = (unsigned short)tid;
+        }
+        __syncthreads();
+        order = by_length;
+    }
+    if (warp == WARPS - 1) {
+        if (lane < kEarly) {
+            int head;
+            const int seq = item_of(a, order, lane, head);
+            plan.early[lane] = seq >= 0 ? load_entry(a, seq) : Entry{-1, 0, 0, 0};
+        }
+        __syncwarp();
+        if (planner) {
+            plan.base = plan.t1 = plan.round = plan.sent = 0;
+            plan.next_seq = item_of(a, order, 0, plan.next_head);
+            for (int n = 0; n < 3; ++n) plan_unit(a, order, plan, units[n], false);
+        }
     }
     __syncthreads();
     bool dead;                                 // the item has no state: its outputs are zero
@@ -348,7 +381,7 @@ slot_steps_kernel(const __grid_constant__ StepArgs a) {
                 }
             }
         }
-        if (planner) plan_unit(a, plan, units[(n + 3) % kPlan], true);
+        if (planner) plan_unit(a, order, plan, units[(n + 3) % kPlan], true);
         fetch_state(units[(n + 1) % kPlan]);
         copy_commit();
 
@@ -362,6 +395,7 @@ slot_steps_kernel(const __grid_constant__ StepArgs a) {
             const bool up = lane & 16, b3 = lane & 8, b2 = lane & 4;
             const int c_own = col + (b3 ? 2 : 0) + (b2 ? 1 : 0);
             const int last = units[n % kPlan].keep - 1;
+#pragma unroll 1                               // two tokens at once spill registers and cost a tenth
             for (int i = 0; i < count; ++i) {
                 Pair r[4], p[4];
 #pragma unroll
@@ -393,7 +427,7 @@ slot_steps_kernel(const __grid_constant__ StepArgs a) {
                 const float mine = (b2 ? y1 : y0) + __shfl_xor_sync(0xffffffffu, b2 ? y0 : y1, 4);
                 const float other = __shfl_xor_sync(0xffffffffu, mine, 16);
                 const float u = s_z[i * DV + c_own] - (up ? other : mine);
-                if (up) s_o[i * DV + c_own] = fmaf(s_kq[i], u, mine);
+                const float out = fmaf(s_kq[i], u, mine);
                 Pair u2[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -407,6 +441,7 @@ slot_steps_kernel(const __grid_constant__ StepArgs a) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) S[j][c] = fma2(k, u2[c], S[j][c]);
                 }
+                if (up) s_o[i * DV + c_own] = out;
                 if (i == last) {
                     float *to = a.pool + ((size_t)units[n % kPlan].slot * a.H + units[n % kPlan].head) * (DK * DV) +
                                 (size_t)(2 * rg) * DV + col;
