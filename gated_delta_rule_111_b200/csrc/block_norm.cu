@@ -16,6 +16,12 @@
 // rings were 5 to 15 % slower).  The dropout's integer work (about 80 instructions
 // per 8 channels) comes before the wait for a row's data.
 //
+// Where D is no multiple of a vector, rows start inside one.  A CTA's rows all start at
+// the same place of a vector, because they are a multiple of 8 rows apart, so its threads
+// take aligned vectors that begin up to 7 channels before the row (SHIFT): a thread's
+// channels stay the same from row to row, and only the vectors at a row's two ends are
+// masked when read and written element by element.
+//
 // Measured on a B200, 16,384 x 2,048, residual scale and p = 0.1: forward, BF16,
 // 49.0 us = 5.48 TB/s (45.7 us without dropout); FP32 stream and BF16 branch 63.9 us
 // = 6.30 TB/s; backward, FP32 stream, 94.3 us = 6.40 TB/s (99 % of a copy's rate), BF16
@@ -30,16 +36,10 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(bf16 x) { return __bfloat162float(x); }
-
-// A vector: V consecutive channels of a row in one thread, as pairs.  Aligned rows (D a
-// multiple of 8) move as whole vectors of V sizeof(T) = 8 or 16 bytes; the lanes of a
-// warp then touch whole sectors of every tensor (8 FP32 channels a lane would leave
-// each access half of a sector).  Other rows go by single elements.
-template <typename TS, typename TB, bool AL> constexpr int vector_channels() {
-    return AL && sizeof(TS) + sizeof(TB) == 4 ? 8 : 4;
-}
+// A vector: V consecutive channels of a row in one thread, as pairs, 8 or 16 bytes of
+// every tensor, so that the lanes of a warp touch whole sectors (8 FP32 channels a lane
+// would leave each access half of a sector).
+template <typename TS, typename TB> constexpr int vector_channels() { return sizeof(TS) + sizeof(TB) == 4 ? 8 : 4; }
 
 template <int BYTES> struct Raw;
 template <> struct Raw<16> { uint4 u; };
@@ -76,14 +76,6 @@ __device__ __forceinline__ void pack(const Pair (&v)[2], Raw<16> &r) {
     r.u = make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
 }
 
-// A pair of FP32 values by its mask word.
-__device__ __forceinline__ Pair mask2(Pair v, uint32_t m) {
-    float a, b;
-    unpack2(v, a, b);
-    return pack2(__uint_as_float(__float_as_uint(a) & __byte_perm(m, 0, 0x1010)),
-                 __uint_as_float(__float_as_uint(b) & __byte_perm(m, 0, 0x3232)));
-}
-
 // Masks V values of type T (one word of m per pair).
 __device__ __forceinline__ void mask(Raw<16> &r, const uint32_t (&m)[4]) { r.u.x &= m[0]; r.u.y &= m[1]; r.u.z &= m[2]; r.u.w &= m[3]; }
 __device__ __forceinline__ void mask(Raw<8> &r, const uint32_t (&m)[2]) { r.u.x &= m[0]; r.u.y &= m[1]; }
@@ -92,87 +84,94 @@ __device__ __forceinline__ void mask(Raw<16> &r, const uint32_t (&m)[2]) {
     r.u.z &= __byte_perm(m[1], 0, 0x1010); r.u.w &= __byte_perm(m[1], 0, 0x3232);
 }
 
-template <typename T, bool AL, int V> __device__ __forceinline__ void load(const T *p, int left, RawOf<T, V> &r, Pair (&v)[V / 2]) {
-    if constexpr (AL) {
-        using U = decltype(r.u);
-        if (left > 0) r.u = __ldcs(reinterpret_cast<const U *>(p));
-    } else {
-        float x[V];
+// The mask words of a vector whose first `skip` channels are the row before's.
+template <int V> __device__ __forceinline__ void inside(int skip, uint32_t (&m)[V / 2]) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) x[e] = e < left ? to_float(__ldcs(p + e)) : 0.f;
-#pragma unroll
-        for (int e = 0; e < V / 2; ++e) v[e] = pack2(x[2 * e], x[2 * e + 1]);
-    }
-}
-template <typename T, bool AL, int V>
-__device__ __forceinline__ void store(T *p, int left, const Pair (&v)[V / 2], const uint32_t (*m)[V / 2] = nullptr) {
-    if constexpr (AL) {
-        RawOf<T, V> r;
-        pack(v, r);
-        if (m) mask(r, *m);
-        if (left > 0) *reinterpret_cast<decltype(r.u) *>(p) = r.u;
-    } else {
-#pragma unroll
-        for (int e = 0; e < V / 2; ++e) {
-            float a, b;
-            unpack2(m ? mask2(v[e], (*m)[e]) : v[e], a, b);
-            if (2 * e < left) Elem<T>::store(p + 2 * e, a);
-            if (2 * e + 1 < left) Elem<T>::store(p + 2 * e + 1, b);
-        }
-    }
+    for (int i = 0; i < V / 2; ++i) m[i] = 2 * i >= skip ? 0xffffffffu : 2 * i + 1 >= skip ? 0xffff0000u : 0u;
 }
 
-// Rows of one tensor on their way to a thread, VPT vectors of each row.  S = 0: in
-// registers, one row ahead.  S > 0: asynchronous copies into shared memory, S rows
-// ahead; a thread reads only what it copied itself, so waiting for its own copies is all
-// the synchronisation there is.  A thread's vector j of a stage lies `at` + j vectors
-// of MAXT threads into the stage.
-template <typename T, bool AL, int V, int VPT, int MAXT, int S> struct Rows {
-    static constexpr int B = V * (int)sizeof(T), BYTES = VPT * MAXT * B;       // of a stage
-    RawOf<T, V> raw[S ? 1 : VPT];
-    Pair val[AL || S ? 1 : VPT][V / 2];
-    const T *base;
-    // Channels past the row's end are zero: set here once, never copied over.
-    __device__ __forceinline__ void init(const T *p, int left, uint32_t at, uint32_t stage_bytes) {
-        base = p;
+// Writes the elements [from, to) of a vector, one of its ends being whole: single halves
+// (BF16), words and pairs of words where they lie.
+__device__ __forceinline__ void store_part(bf16 *p, const Raw<8> &r, int from, int to) {
+    const uint32_t w[2] = {r.u.x, r.u.y};
+    if (from & 1) reinterpret_cast<uint16_t *>(p)[from] = (uint16_t)((from & 2 ? w[1] : w[0]) >> 16);
+    if (to & 1) reinterpret_cast<uint16_t *>(p)[to - 1] = (uint16_t)(to & 2 ? w[1] : w[0]);
+    if (from <= 0 && to >= 2) reinterpret_cast<uint32_t *>(p)[0] = w[0];
+    if (from <= 2 && to >= 4) reinterpret_cast<uint32_t *>(p)[1] = w[1];
+}
+__device__ __forceinline__ void store_part(bf16 *p, const Raw<16> &r, int from, int to) {
+    const uint32_t w[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
+    if (from & 1) reinterpret_cast<uint16_t *>(p)[from] = (uint16_t)((from & 4 ? from & 2 ? w[3] : w[2] : from & 2 ? w[1] : w[0]) >> 16);
+    if (to & 1) reinterpret_cast<uint16_t *>(p)[to - 1] = (uint16_t)(to & 4 ? to & 2 ? w[3] : w[2] : to & 2 ? w[1] : w[0]);
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            if constexpr (S > 0) {
-                if (left <= j * (int)blockDim.x * V)
-                    for (int i = 0; i < S; ++i)
-                        zero_shared<B>(at + i * stage_bytes + threadIdx.x * B + j * MAXT * B);
-            } else if constexpr (AL) {
-                raw[j] = {};
-            }
-        }
+    for (int i = 0; i < 4; ++i)
+        if (from <= 2 * i && to >= 2 * i + 2) reinterpret_cast<uint32_t *>(p)[i] = w[i];
+}
+__device__ __forceinline__ void store_part(float *p, const Raw<16> &r, int from, int to) {
+    const uint32_t w[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (from <= i && to >= i + 1) reinterpret_cast<uint32_t *>(p)[i] = w[i];
+}
+
+// Writes a vector to p, channels c and on of its row; where it reaches beyond the row (SHIFT),
+// the channels of the row alone.
+template <typename T, int V, bool SHIFT>
+__device__ __forceinline__ void store(T *p, int c, int D, const Pair (&v)[V / 2], const uint32_t (*m)[V / 2] = nullptr) {
+    RawOf<T, V> r;
+    pack(v, r);
+    if (m) mask(r, *m);
+    if (c >= D) return;
+    if (SHIFT && (c < 0 || c + V > D))
+        store_part(p, r, c < 0 ? -c : 0, min(V, D - c));
+    else
+        *reinterpret_cast<decltype(r.u) *>(p) = r.u;
+}
+
+// Rows of one tensor on their way to a thread, VPT vectors of each row, by asynchronous
+// copies into shared memory, S rows ahead.  A thread reads only what it copied itself, so
+// waiting for its own copies is all the synchronisation there is.  A thread's vector j of
+// a stage lies `at` + j vectors of MAXT threads into the stage; its first channel is
+// c0 + j blockDim V.
+template <typename T, int V, int VPT, int MAXT, int S, bool SHIFT> struct Rows {
+    static constexpr int B = V * (int)sizeof(T), BYTES = VPT * MAXT * B;       // of a stage
+    const T *base;
+    int c0, D;
+    // Vectors past the row's end are zero: set here once, never copied over.
+    __device__ __forceinline__ void init(const T *p, int c, int d, uint32_t at, uint32_t stage_bytes) {
+        base = p;
+        c0 = c;
+        D = d;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (c0 + j * (int)blockDim.x * V >= D)
+                for (int i = 0; i < S; ++i) zero_shared<B>(at + i * stage_bytes + threadIdx.x * B + j * MAXT * B);
     }
-    // `e`: the element offset of the thread's first vector; `left`: channels from there to the row's end
-    __device__ __forceinline__ void fetch(size_t e, int left, uint32_t at) {
+    // `e`: the element offset of the thread's first vector.  Past a row's end nothing is read (the last
+    // row's may be the tensor's).
+    __device__ __forceinline__ void fetch(size_t e, uint32_t at) {
         if (!base) return;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int skip = j * (int)blockDim.x * V;
-            if constexpr (S > 0) {
-                if (left > skip) copy_async<B>(at + threadIdx.x * B + j * MAXT * B, base + e + skip);
-            } else {
-                load<T, AL, V>(base + e + skip, left - skip, raw[j], val[AL ? 0 : j]);
-            }
+            const int c = c0 + j * (int)blockDim.x * V;
+            const uint32_t to = at + threadIdx.x * B + j * MAXT * B;
+            if (c >= D) continue;
+            if (SHIFT && c + V > D)
+                copy_async_part<B>(to, base + e + j * (int)blockDim.x * V, (D - c) * (int)sizeof(T));
+            else
+                copy_async<B>(to, base + e + j * (int)blockDim.x * V);
         }
     }
-    __device__ __forceinline__ void read(int j, uint32_t at, Pair (&v)[V / 2],
-                                         const uint32_t (*m)[V / 2] = nullptr) {
-        if constexpr (AL) {
-            RawOf<T, V> r;
-            if constexpr (S > 0)
-                load_shared(at + threadIdx.x * B + j * MAXT * B, r.u);
-            else
-                r = raw[j];
-            if (m) mask(r, *m);
-            unpack(r, v);
-        } else {
-#pragma unroll
-            for (int e = 0; e < V / 2; ++e) v[e] = m ? mask2(val[j][e], (*m)[e]) : val[j][e];
+    __device__ __forceinline__ void read(int j, uint32_t at, Pair (&v)[V / 2], const uint32_t (*m)[V / 2] = nullptr) {
+        RawOf<T, V> r;
+        load_shared(at + threadIdx.x * B + j * MAXT * B, r.u);
+        if (m) mask(r, *m);
+        if (SHIFT && c0 < 0 && j == 0) {           // the row before, in the first thread's vector
+            uint32_t in[V / 2];
+            inside<V>(-c0, in);
+            mask(r, in);
         }
+        unpack(r, v);
     }
 };
 
@@ -182,15 +181,15 @@ template <typename T, bool AL, int V, int VPT, int MAXT, int S> struct Rows {
 template <int V, int VPT, int MAXT, bool SHARED> struct Channels {
     Pair reg[SHARED ? 1 : VPT][V / 2];
     uint32_t at;
-    __device__ __forceinline__ void init(const float *p, uint32_t smem, int D, float fill, float factor) {
+    __device__ __forceinline__ void init(const float *p, uint32_t smem, int c0, int D, float fill, float factor) {
         at = smem + threadIdx.x * 16;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = (j * (int)blockDim.x + (int)threadIdx.x) * V;
+            const int c = c0 + j * (int)blockDim.x * V;
+            auto channel = [&](int at) { return (p && at >= 0 && at < D ? __ldg(p + at) : fill) * factor; };
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
-                const Pair x = pack2((p && c + 2 * i < D ? __ldg(p + c + 2 * i) : fill) * factor,
-                                     (p && c + 2 * i + 1 < D ? __ldg(p + c + 2 * i + 1) : fill) * factor);
+                const Pair x = pack2(channel(c + 2 * i), channel(c + 2 * i + 1));
                 if constexpr (SHARED)
                     store_shared(at + (j * V / 4 + i / 2) * MAXT * 16 + i % 2 * 8, x.v);
                 else
@@ -217,7 +216,10 @@ template <int MAXT> __device__ __forceinline__ float cta_sum(float x, float *buf
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
     const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-    if (warps == 1) return x;
+    if (warps == 1) {
+        __syncwarp();                       // as the barrier for what lanes leave to one another
+        return x;
+    }
     if (lane == 0) buf[threadIdx.x >> 5] = x;
     __syncthreads();
     x = (lane & (MAXT / 32 - 1)) < warps ? buf[lane & (MAXT / 32 - 1)] : 0.f;
@@ -229,29 +231,66 @@ template <int MAXT> __device__ __forceinline__ float cta_sum(float x, float *buf
 // Which channels of a thread's vectors a row keeps: one word per pair, its low half ones
 // for the first channel and its high half for the second.  Two BF16 values are masked
 // by one operation, and a dropped value leaves nothing, whatever it was.
-template <int V, int VPT> struct Keep {
-    philox::Lane lane[VPT * V / 4];
-    uint32_t m[VPT][V / 2];
-    __device__ __forceinline__ void init(const Dropout &dp, uint2 key, uint2 offset, int c0) {
-        if (dp.rng)
+//
+// Vector j of a thread is vector n = j blockDim + threadIdx of the row.  The thread draws
+// channels n V to n V + V - 1.  Where rows are not shifted, those are the vector's.  Where
+// they are, its first `skip` channels are the last ones that vector n - 1 drew: a lane gets
+// them from the lane before, and the first lane of a warp from shared memory, where the
+// last lane of the warp before left them.  So a shifted row's channels are drawn
+// (start) before the barrier of the row before it, and put together (finish) after it.
+template <int V, int VPT, bool SHIFT> struct Keep {
+    static constexpr int GROUPS = V / 4;               // groups of four channels
+    philox::Lane lane[VPT][GROUPS];
+    uint32_t m[VPT][V / 2], drawn[SHIFT ? VPT : 1];
+    __device__ __forceinline__ void init(const Dropout &dp, uint2 key, uint2 offset) {
 #pragma unroll
-            for (int q = 0; q < VPT * V / 4; ++q) {
-                const int c = c0 + q / (V / 4) * (int)blockDim.x * V + q % (V / 4) * 4;
-                lane[q] = philox::lane_for((uint32_t)c >> 2, key, offset);
-            }
+        for (int j = 0; j < VPT; ++j) {
+            const int first = (j * (int)blockDim.x + (int)threadIdx.x) * GROUPS;
+            if (dp.rng)
 #pragma unroll
-        for (int j = 0; j < VPT; ++j)
+                for (int q = 0; q < GROUPS; ++q) lane[j][q] = philox::lane_for((uint32_t)(first + q), key, offset);
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) m[j][i] = 0xffffffffu;
+        }
     }
     __device__ __forceinline__ void draw(const Dropout &dp, uint2 key, uint2 offset, int row) {
         const philox::Row r = philox::row_for((uint32_t)row, key, offset);
 #pragma unroll
-        for (int q = 0; q < VPT * V / 4; ++q) {
-            const uint4 w = philox::words(lane[q], r, key);
-            uint32_t *to = m[q / (V / 4)] + q % (V / 4) * 2;
-            to[0] = (w.x >= dp.threshold ? 0xffffu : 0u) | (w.y >= dp.threshold ? 0xffff0000u : 0u);
-            to[1] = (w.z >= dp.threshold ? 0xffffu : 0u) | (w.w >= dp.threshold ? 0xffff0000u : 0u);
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int q = 0; q < GROUPS; ++q) {
+                const uint4 w = philox::words(lane[j][q], r, key);
+                m[j][2 * q] = (w.x >= dp.threshold ? 0xffffu : 0u) | (w.y >= dp.threshold ? 0xffff0000u : 0u);
+                m[j][2 * q + 1] = (w.z >= dp.threshold ? 0xffffu : 0u) | (w.w >= dp.threshold ? 0xffff0000u : 0u);
+            }
+    }
+    // `left`: a word per vector and warp of shared memory, another one from row to row
+    __device__ __forceinline__ void start(const Dropout &dp, uint2 key, uint2 offset, int row, uint32_t (*left)[32]) {
+        const philox::Row r = philox::row_for((uint32_t)row, key, offset);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            uint32_t bits = 0;
+#pragma unroll
+            for (int q = 0; q < GROUPS; ++q) {
+                const uint4 w = philox::words(lane[j][q], r, key);
+                bits |= (w.x >= dp.threshold ? 1u << 4 * q : 0u) | (w.y >= dp.threshold ? 2u << 4 * q : 0u) |
+                        (w.z >= dp.threshold ? 4u << 4 * q : 0u) | (w.w >= dp.threshold ? 8u << 4 * q : 0u);
+            }
+            drawn[j] = bits;
+            if ((threadIdx.x & 31) == 31) left[j][threadIdx.x >> 5] = bits;
+        }
+    }
+    __device__ __forceinline__ void finish(int skip, const uint32_t (*left)[32]) {
+        const int warp = threadIdx.x >> 5;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            uint32_t before = __shfl_up_sync(0xffffffffu, drawn[j], 1);
+            if ((threadIdx.x & 31) == 0)
+                before = warp > 0 ? left[j][warp - 1] : j > 0 ? left[j - 1][(blockDim.x >> 5) - 1] : 0u;
+            const uint32_t bits = (drawn[j] << V | before) >> (V - skip);
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i)
+                m[j][i] = (bits >> 2 * i & 1 ? 0xffffu : 0u) | (bits >> 2 * i & 2 ? 0xffff0000u : 0u);
         }
     }
 };
@@ -264,48 +303,60 @@ __device__ __forceinline__ void rng_words(const Dropout &dp, uint2 &key, uint2 &
     offset = make_uint2((uint32_t)o, (uint32_t)(o >> 32));
 }
 
-template <typename TS, typename TB, bool AL, int VPT, int MAXT, int S>
+template <typename TS, typename TB, bool SHIFT, int VPT, int MAXT, int S>
 __global__ void __launch_bounds__(MAXT, 1024 / MAXT)
 residual_norm_kernel(const TS *x, const TB *r, const float *__restrict__ weight, const float *__restrict__ scale,
                      Dropout dp, float eps, TS *h, TB *y, float *__restrict__ rstd, int rows, int D) {
-    constexpr int V = vector_channels<TS, TB, AL>(), P = V / 2;
-    using RS = Rows<TS, AL, V, VPT, MAXT, S>;
-    using RB = Rows<TB, AL, V, VPT, MAXT, S>;
+    constexpr int V = vector_channels<TS, TB>(), P = V / 2;
+    using RS = Rows<TS, V, VPT, MAXT, S, SHIFT>;
+    using RB = Rows<TB, V, VPT, MAXT, S, SHIFT>;
     constexpr uint32_t kStage = RS::BYTES + RB::BYTES;
     extern __shared__ uint4 ring[];
     __shared__ float red[2][32];
+    __shared__ uint32_t left[2][SHIFT ? VPT : 1][32];
     const uint32_t ring0 = smem_address(ring);
     uint2 key, offset;
     rng_words(dp, key, offset);
-    const int grid = gridDim.x, c0 = threadIdx.x * V, left = D - c0;
+    const int grid = gridDim.x;
+    // the CTA's rows start `skip` channels into a vector
+    const int skip = SHIFT ? (int)((size_t)blockIdx.x * D % V) : 0, c0 = threadIdx.x * V - skip;
     RS rx;
     RB rr;
-    rx.init(x, left, ring0, kStage);
-    rr.init(r, left, ring0 + RS::BYTES, kStage);
+    rx.init(x, c0, D, ring0, kStage);
+    rr.init(r, c0, D, ring0 + RS::BYTES, kStage);
     const size_t step = (size_t)grid * D;
     int row = blockIdx.x, ahead = row;                  // the row in hand and the next one to fetch
     size_t e = (size_t)row * D + c0, e_ahead = e;
     auto fetch = [&](uint32_t at) {
         if (ahead < rows) {
-            rx.fetch(e_ahead, left, at);
-            rr.fetch(e_ahead, left, at + RS::BYTES);
+            rx.fetch(e_ahead, at);
+            rr.fetch(e_ahead, at + RS::BYTES);
         }
         ahead = ahead < rows ? ahead + grid : ahead;
         e_ahead += step;
-        if constexpr (S > 0) copy_commit();
+        copy_commit();
     };
 #pragma unroll
-    for (int i = 0; i < (S ? S : 1); ++i) fetch(ring0 + i * kStage);
+    for (int i = 0; i < S; ++i) fetch(ring0 + i * kStage);
     Channels<V, VPT, MAXT, false> wt, sc;
-    wt.init(weight, 0, D, 0.f, 1.f);
-    sc.init(scale, 0, D, 1.f, dp.inv_keep);
-    Keep<V, VPT> keep;
-    keep.init(dp, key, offset, c0);
+    wt.init(weight, 0, c0, D, 0.f, 1.f);
+    sc.init(scale, 0, c0, D, 1.f, dp.inv_keep);
+    Keep<V, VPT, SHIFT> keep;
+    keep.init(dp, key, offset);
+    if (SHIFT && dp.rng) {
+        keep.start(dp, key, offset, row, left[0]);
+        __syncthreads();
+    }
     const float inv_d = 1.f / (float)D;
     uint32_t at = ring0;
     for (int it = 0; row < rows; row += grid, it ^= 1) {
-        if (dp.rng) keep.draw(dp, key, offset, row);    // before the wait: needs no data
-        if constexpr (S > 0) copy_wait<S ? S - 1 : 0>();
+        if (dp.rng) {                               // before the wait: needs no data
+            if constexpr (SHIFT)
+                keep.finish(skip, left[it]);
+            else
+                keep.draw(dp, key, offset, row);
+        }
+        copy_wait<S - 1>();
         Pair hv[VPT][P], ss2 = pack2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -321,7 +372,8 @@ residual_norm_kernel(const TS *x, const TB *r, const float *__restrict__ weight,
             for (int i = 0; i < P; ++i) ss2 = fma2(hv[j][i], hv[j][i], ss2);
         }
         fetch(at);                                  // this thread's part of the stage has been read
-        if constexpr (S > 0) at = at == ring0 + (S - 1) * kStage ? ring0 : at + kStage;
+        at = at == ring0 + (S - 1) * kStage ? ring0 : at + kStage;
+        if (SHIFT && dp.rng && row < rows - grid) keep.start(dp, key, offset, row + grid, left[it ^ 1]);
         float s0, s1;
         unpack2(ss2, s0, s1);
         const float rs = rsqrtf(cta_sum<MAXT>(s0 + s1, red[it]) * inv_d + eps);
@@ -329,13 +381,13 @@ residual_norm_kernel(const TS *x, const TB *r, const float *__restrict__ weight,
         const Pair rs2 = pack2(rs, rs);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int skip = j * (int)blockDim.x * V;
-            if (h) store<TS, AL, V>(h + e + skip, left - skip, hv[j]);
+            const int c = c0 + j * (int)blockDim.x * V;
+            if (h) store<TS, V, SHIFT>(h + e + (c - c0), c, D, hv[j]);
             Pair w[P];
             wt.get(j, w);
 #pragma unroll
             for (int i = 0; i < P; ++i) hv[j][i] = mul2(mul2(hv[j][i], rs2), w[i]);
-            store<TB, AL, V>(y + e + skip, left - skip, hv[j]);
+            store<TB, V, SHIFT>(y + e + (c - c0), c, D, hv[j]);
         }
         e += step;
         if (row >= rows - grid) break;              // row + grid may pass 2^31
@@ -348,65 +400,77 @@ residual_norm_kernel(const TS *x, const TB *r, const float *__restrict__ weight,
 // A CTA adds its rows' shares of the two sums in registers and writes them to its
 // row of `part` ([gridDim][1 or 2][D]); reduce_parts_kernel adds those in a fixed
 // order, so the result does not change from call to call.
-template <typename TS, typename TB, bool AL, int VPT, int MAXT, int S>
+template <typename TS, typename TB, bool SHIFT, int VPT, int MAXT, int S>
 __global__ void __launch_bounds__(MAXT, MAXT <= 512 ? 512 / MAXT : 1)
 residual_norm_bwd_kernel(const TB *__restrict__ dy, const TS *__restrict__ h, const float *__restrict__ rstd,
                          const float *__restrict__ weight, const TS *dh, const TB *__restrict__ r,
                          const float *__restrict__ scale, Dropout dp, TS *dx, TB *__restrict__ dr,
                          float *__restrict__ part, int rows, int D) {
-    constexpr int V = vector_channels<TS, TB, AL>(), P = V / 2;
-    using RS = Rows<TS, AL, V, VPT, MAXT, S>;
-    using RB = Rows<TB, AL, V, VPT, MAXT, S>;
-    using C = Channels<V, VPT, MAXT, (MAXT > 512 && S > 0)>;
+    constexpr int V = vector_channels<TS, TB>(), P = V / 2;
+    using RS = Rows<TS, V, VPT, MAXT, S, SHIFT>;
+    using RB = Rows<TB, V, VPT, MAXT, S, SHIFT>;
+    using C = Channels<V, VPT, MAXT, (MAXT > 512 && VPT * V == 8)>;
     constexpr uint32_t kDh = RS::BYTES, kDy = 2 * RS::BYTES, kR = kDy + RB::BYTES, kStage = kR + RB::BYTES;
     extern __shared__ uint4 ring[];
     __shared__ float red[2][32];
+    __shared__ uint32_t left[2][SHIFT ? VPT : 1][32];
     cudaTriggerProgrammaticLaunchCompletion();       // the sums' launch may be set up; it waits for this grid's end
     const uint32_t ring0 = smem_address(ring);
     uint2 key, offset;
     rng_words(dp, key, offset);
     RB rdy, rr;
     RS rh, rdh;
-    const int grid = gridDim.x, c0 = threadIdx.x * V, left = D - c0;
-    rdy.init(dy, left, ring0 + kDy, kStage);
-    rr.init(r, left, ring0 + kR, kStage);
-    rh.init(h, left, ring0, kStage);
-    rdh.init(dh, left, ring0 + kDh, kStage);
+    const int grid = gridDim.x;
+    // the CTA's rows start `skip` channels into a vector
+    const int skip = SHIFT ? (int)((size_t)blockIdx.x * D % V) : 0, c0 = threadIdx.x * V - skip;
+    rdy.init(dy, c0, D, ring0 + kDy, kStage);
+    rr.init(r, c0, D, ring0 + kR, kStage);
+    rh.init(h, c0, D, ring0, kStage);
+    rdh.init(dh, c0, D, ring0 + kDh, kStage);
     const size_t step = (size_t)grid * D;
     int row = blockIdx.x, ahead = row;                  // the row in hand and the next one to fetch
     size_t e = (size_t)row * D + c0, e_ahead = e;
     auto fetch = [&](uint32_t at) {
         if (ahead < rows) {
-            rdy.fetch(e_ahead, left, at + kDy);
-            rh.fetch(e_ahead, left, at);
-            rdh.fetch(e_ahead, left, at + kDh);
-            rr.fetch(e_ahead, left, at + kR);
+            rdy.fetch(e_ahead, at + kDy);
+            rh.fetch(e_ahead, at);
+            rdh.fetch(e_ahead, at + kDh);
+            rr.fetch(e_ahead, at + kR);
         }
         ahead = ahead < rows ? ahead + grid : ahead;
         e_ahead += step;
-        if constexpr (S > 0) copy_commit();
+        copy_commit();
     };
 #pragma unroll
-    for (int i = 0; i < (S ? S : 1); ++i) fetch(ring0 + i * kStage);
+    for (int i = 0; i < S; ++i) fetch(ring0 + i * kStage);
     float rs_next = __ldg(rstd + row);
     C wt, sc;
-    wt.init(weight, ring0 + S * kStage, D, 0.f, 1.f);
-    sc.init(scale, ring0 + S * kStage + VPT * MAXT * V * 4, D, 1.f, dp.inv_keep);
+    wt.init(weight, ring0 + S * kStage, c0, D, 0.f, 1.f);
+    sc.init(scale, ring0 + S * kStage + VPT * MAXT * V * 4, c0, D, 1.f, dp.inv_keep);
     Pair aw[VPT][P], as[VPT][P];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
 #pragma unroll
         for (int i = 0; i < P; ++i) aw[j][i] = as[j][i] = pack2(0.f, 0.f);
     }
-    Keep<V, VPT> keep;
-    keep.init(dp, key, offset, c0);
+    Keep<V, VPT, SHIFT> keep;
+    keep.init(dp, key, offset);
+    if (SHIFT && dp.rng) {
+        keep.start(dp, key, offset, row, left[0]);
+        __syncthreads();
+    }
     const float inv_d = 1.f / (float)D;
     uint32_t at = ring0;
     for (int it = 0; row < rows; row += grid, it ^= 1) {
-        if (dp.rng) keep.draw(dp, key, offset, row);    // before the wait: needs no data
+        if (dp.rng) {                               // before the wait: needs no data
+            if constexpr (SHIFT)
+                keep.finish(skip, left[it]);
+            else
+                keep.draw(dp, key, offset, row);
+        }
         const float rs = rs_next;
         const Pair rs2 = pack2(rs, rs);
-        if constexpr (S > 0) copy_wait<S ? S - 1 : 0>();
+        copy_wait<S - 1>();
         Pair n[VPT][P], t[VPT][P], gx[VPT][P], b[VPT][P], dot2 = pack2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -424,6 +488,7 @@ residual_norm_bwd_kernel(const TB *__restrict__ dy, const TS *__restrict__ h, co
         }
         const bool last = row >= rows - grid;
         if (!last) rs_next = __ldg(rstd + row + grid);
+        if (SHIFT && dp.rng && !last) keep.start(dp, key, offset, row + grid, left[it ^ 1]);
         float d0, d1;
         unpack2(dot2, d0, d1);
         const float mean = -cta_sum<MAXT>(d0 + d1, red[it]) * inv_d;
@@ -437,13 +502,13 @@ residual_norm_bwd_kernel(const TB *__restrict__ dy, const TS *__restrict__ h, co
                 if (!dh) gx[j][i] = pack2(0.f, 0.f);
         }
         fetch(at);                                  // this thread's part of the stage has been read
-        if constexpr (S > 0) at = at == ring0 + (S - 1) * kStage ? ring0 : at + kStage;
+        at = at == ring0 + (S - 1) * kStage ? ring0 : at + kStage;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int skip = j * (int)blockDim.x * V;
+            const int c = c0 + j * (int)blockDim.x * V;
 #pragma unroll
             for (int i = 0; i < P; ++i) gx[j][i] = fma2(rs2, fma2(n[j][i], mean2, t[j][i]), gx[j][i]);
-            store<TS, AL, V>(dx + e + skip, left - skip, gx[j]);
+            store<TS, V, SHIFT>(dx + e + (c - c0), c, D, gx[j]);
             if (r) {                                // as is scaled by 1 / (1 - p) at the end
 #pragma unroll
                 for (int i = 0; i < P; ++i) as[j][i] = fma2(gx[j][i], b[j][i], as[j][i]);
@@ -453,7 +518,7 @@ residual_norm_bwd_kernel(const TB *__restrict__ dy, const TS *__restrict__ h, co
                 sc.get(j, s);
 #pragma unroll
                 for (int i = 0; i < P; ++i) gx[j][i] = mul2(gx[j][i], s[i]);
-                store<TB, AL, V>(dr + e + skip, left - skip, gx[j], &keep.m[j]);
+                store<TB, V, SHIFT>(dr + e + (c - c0), c, D, gx[j], &keep.m[j]);
             }
         }
         e += step;
@@ -468,11 +533,11 @@ residual_norm_bwd_kernel(const TB *__restrict__ dy, const TS *__restrict__ h, co
             float a0, a1, s0, s1;
             unpack2(aw[j][i], a0, a1);
             unpack2(as[j][i], s0, s1);
-            if (c + 2 * i < D) {
+            if (c + 2 * i >= 0 && c + 2 * i < D) {
                 pw[c + 2 * i] = a0;
                 if (r) pw[D + c + 2 * i] = s0 * dp.inv_keep;
             }
-            if (c + 2 * i + 1 < D) {
+            if (c + 2 * i + 1 >= 0 && c + 2 * i + 1 < D) {
                 pw[c + 2 * i + 1] = a1;
                 if (r) pw[D + c + 2 * i + 1] = s1 * dp.inv_keep;
             }
@@ -511,27 +576,27 @@ int device_sms() {
     return sms;
 }
 
-// How a width is split over a CTA: 8 channels a thread up to 8,192 (aligned, through the
-// shared-memory ring) or 4 up to 4,096 (not aligned); more channels a thread, in
-// registers, beyond.
+// How a width is split over a CTA: 8 channels a thread up to 8,192; a few shifted widths
+// below that need one vector more.
 struct Split {
     int threads;
-    bool aligned, wide;
+    bool shift, more;
 };
-Split split_for(int D) {
-    Split s{0, D % 8 == 0, false};
-    int per = s.aligned ? 8 : 4;
-    s.wide = D > per * 1024;
-    if (s.wide) per *= s.aligned ? 2 : 4;
-    s.threads = ((D + per - 1) / per + 31) / 32 * 32;
+Split split_for(int D, int V) {
+    Split s{0, D % V != 0, false};
+    const int vectors = s.shift ? (D + 2 * V - 2) / V : D / V, k = 8 / V;
+    s.more = vectors > 1024 * k;
+    s.threads = s.more ? 1024 : ((vectors + k - 1) / k + 31) / 32 * 32;
     return s;
 }
 
-// CTAs per SM: 1,024 threads of the forward (64 registers each), 512 of the backward
-// (its two sums' accumulators take 128).
-int grid_for(int rows, int threads, int per_sm, int sms) {
-    const int ctas = threads >= per_sm ? 1 : per_sm / threads;
-    const long long cap = (long long)sms * ctas;
+// CTAs: as many as an SM holds (`per_sm` threads: 1,024 of the forward, 64 registers each, or 512
+// of the backward, whose two sums' accumulators take 128).  Shifted rows want a multiple of
+// 8 where a CTA gets several, so that they all start at the same place of a vector.
+int grid_for(int rows, const Split &s, int per_sm, int sms) {
+    const int ctas = s.threads >= per_sm ? 1 : per_sm / s.threads;
+    long long cap = (long long)sms * ctas;
+    if (s.shift) cap = cap > 8 ? cap / 8 * 8 : 8;
     return (int)(rows < cap ? rows : cap);
 }
 
@@ -551,15 +616,15 @@ struct FwdArgs {
     int rows, D;
 };
 
-template <typename TS, typename TB, bool AL, int VPT, int MAXT, bool RING>
-cudaError_t fwd_launch(const FwdArgs &a, int threads, cudaStream_t st) {
-    constexpr int bytes = VPT * vector_channels<TS, TB, AL>() * (int)(sizeof(TS) + sizeof(TB));
-    constexpr int S = RING ? 1 : 0;          // 32 to 64 KB in flight an SM; two rows ahead measured slower
-    auto kernel = residual_norm_kernel<TS, TB, AL, VPT, MAXT, S>;
+template <typename TS, typename TB, bool SHIFT, int VPT, int MAXT>
+cudaError_t fwd_launch(const FwdArgs &a, const Split &s, cudaStream_t st) {
+    constexpr int bytes = VPT * vector_channels<TS, TB>() * (int)(sizeof(TS) + sizeof(TB));
+    constexpr int S = 1;                     // 32 to 64 KB in flight an SM; two rows ahead measured slower
+    auto kernel = residual_norm_kernel<TS, TB, SHIFT, VPT, MAXT, S>;
     const size_t smem = (size_t)MAXT * bytes * S;
     const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid_for(a.rows, threads, 1024, device_sms()), threads, smem, st>>>(
+    kernel<<<grid_for(a.rows, s, 1024, device_sms()), s.threads, smem, st>>>(
         static_cast<const TS *>(a.x), static_cast<const TB *>(a.r), a.weight, a.scale, a.dp, a.eps,
         static_cast<TS *>(a.h), static_cast<TB *>(a.y), a.rstd, a.rows, a.D);
     return cudaGetLastError();
@@ -576,17 +641,17 @@ struct BwdArgs {
     int rows, D, grid;
 };
 
-template <typename TS, typename TB, bool AL, int VPT, int MAXT, bool RING>
-cudaError_t bwd_launch(const BwdArgs &a, int threads, cudaStream_t st) {
-    constexpr int bytes = VPT * vector_channels<TS, TB, AL>() * 2 * (int)(sizeof(TS) + sizeof(TB));
+template <typename TS, typename TB, bool SHIFT, int VPT, int MAXT>
+cudaError_t bwd_launch(const BwdArgs &a, const Split &s, cudaStream_t st) {
+    constexpr int bytes = VPT * vector_channels<TS, TB>() * 2 * (int)(sizeof(TS) + sizeof(TB));
     // Two rows in flight where that is at most 96 KB an SM, else one: more measured slower.
-    constexpr int S = RING ? (2 * bytes * (MAXT > 512 ? MAXT : 512) <= 98304 ? 2 : 1) : 0;
-    auto kernel = residual_norm_bwd_kernel<TS, TB, AL, VPT, MAXT, S>;
-    constexpr bool shared_channels = MAXT > 512 && S > 0;      // weight and scale, see Channels
+    constexpr int S = 2 * bytes * (MAXT > 512 ? MAXT : 512) <= 98304 ? 2 : 1;
+    auto kernel = residual_norm_bwd_kernel<TS, TB, SHIFT, VPT, MAXT, S>;
+    constexpr bool shared_channels = MAXT > 512 && VPT * vector_channels<TS, TB>() == 8;     // weight and scale, see Channels
     const size_t smem = (size_t)MAXT * (bytes * S + (shared_channels ? 2 * 8 * 4 : 0));
     const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<a.grid, threads, smem, st>>>(
+    kernel<<<a.grid, s.threads, smem, st>>>(
         static_cast<const TB *>(a.dy), static_cast<const TS *>(a.h), a.rstd, a.weight, static_cast<const TS *>(a.dh),
         static_cast<const TB *>(a.r), a.scale, a.dp, static_cast<TS *>(a.dx), static_cast<TB *>(a.dr), a.part, a.rows,
         a.D);
@@ -594,18 +659,20 @@ cudaError_t bwd_launch(const BwdArgs &a, int threads, cudaStream_t st) {
 }
 
 // The instance of LAUNCH (fwd_launch, bwd_launch) that a width needs; k vectors make 8 channels.
+#define GDN2_BY_THREADS(LAUNCH, SHIFT)                                                         \
+    {                                                                                          \
+        if (s.threads <= 64) return LAUNCH<TS, TB, SHIFT, k, 64>(a, s, st);            \
+        if (s.threads <= 128) return LAUNCH<TS, TB, SHIFT, k, 128>(a, s, st);          \
+        if (s.threads <= 256) return LAUNCH<TS, TB, SHIFT, k, 256>(a, s, st);          \
+        if (s.threads <= 512) return LAUNCH<TS, TB, SHIFT, k, 512>(a, s, st);          \
+        return LAUNCH<TS, TB, SHIFT, k, 1024>(a, s, st);                               \
+    }
 #define GDN2_BY_WIDTH(LAUNCH)                                                                  \
-    constexpr int k = 8 / vector_channels<TS, TB, true>();                                     \
-    const Split s = split_for(a.D);                                                            \
-    if (s.aligned && !s.wide) {                                                                \
-        if (s.threads <= 64) return LAUNCH<TS, TB, true, k, 64, true>(a, s.threads, st);       \
-        if (s.threads <= 256) return LAUNCH<TS, TB, true, k, 256, true>(a, s.threads, st);     \
-        if (s.threads <= 512) return LAUNCH<TS, TB, true, k, 512, true>(a, s.threads, st);     \
-        return LAUNCH<TS, TB, true, k, 1024, true>(a, s.threads, st);                          \
-    }                                                                                          \
-    if (s.aligned) return LAUNCH<TS, TB, true, 2 * k, 1024, false>(a, s.threads, st);          \
-    if (s.wide) return LAUNCH<TS, TB, false, 4, 1024, false>(a, s.threads, st);                \
-    return LAUNCH<TS, TB, false, 1, 1024, false>(a, s.threads, st);
+    constexpr int V = vector_channels<TS, TB>(), k = 8 / V;                                    \
+    const Split s = split_for(a.D, V);                                                         \
+    if (s.more) return LAUNCH<TS, TB, true, k + 1, 1024>(a, s, st);                    \
+    if (s.shift) GDN2_BY_THREADS(LAUNCH, true)                                                 \
+    GDN2_BY_THREADS(LAUNCH, false)
 
 template <typename TS, typename TB> cudaError_t fwd_sized(const FwdArgs &a, cudaStream_t st) {
     GDN2_BY_WIDTH(fwd_launch)
@@ -614,10 +681,16 @@ template <typename TS, typename TB> cudaError_t bwd_sized(const BwdArgs &a, cuda
     GDN2_BY_WIDTH(bwd_launch)
 }
 #undef GDN2_BY_WIDTH
+#undef GDN2_BY_THREADS
 
 // CTAs of the backward: the workspace holds one row of partial sums for each, so
 // the count goes by the sizes alone (148 SMs).
-int bwd_grid(int rows, int D) { return grid_for(rows, split_for(D).threads, 512, 148); }
+int bwd_grid(int rows, int D, int V) { return grid_for(rows, split_for(D, V), 512, 148); }
+int vector_of(gdn2_dtype stream_dt, gdn2_dtype dt) {
+    return stream_dt == GDN2_BF16 ? vector_channels<bf16, bf16>()
+           : dt == GDN2_BF16      ? vector_channels<float, bf16>()
+                                  : vector_channels<float, float>();
+}
 
 }  // namespace
 
@@ -645,8 +718,9 @@ cudaError_t launch_residual_norm(const void *x, const void *r, const float *weig
     return dt == GDN2_BF16 ? fwd_sized<float, bf16>(a, st) : fwd_sized<float, float>(a, st);
 }
 
-size_t residual_norm_bwd_workspace_bytes(int rows, int D) {
-    return (size_t)bwd_grid(rows, D) * 2 * D * sizeof(float);
+size_t residual_norm_bwd_workspace_bytes(int rows, int D) {       // whatever the types
+    const int a = bwd_grid(rows, D, 4), b = bwd_grid(rows, D, 8);
+    return (size_t)(a > b ? a : b) * 2 * D * sizeof(float);
 }
 
 cudaError_t launch_residual_norm_bwd(const void *dy, const void *h, const float *rstd, const float *weight,
@@ -655,7 +729,7 @@ cudaError_t launch_residual_norm_bwd(const void *dy, const void *h, const float 
                                      float *workspace, int rows, int D, gdn2_dtype stream_dt, gdn2_dtype dt,
                                      cudaStream_t st) {
     const Dropout dp{p > 0.0 ? rng : nullptr, (uint32_t)(p * 4294967296.0), (float)(1.0 / (1.0 - p))};
-    const int grid = bwd_grid(rows, D);
+    const int grid = bwd_grid(rows, D, vector_of(stream_dt, dt));
     const bool direct = grid == 1 && !dscale;          // one CTA's sums are the result
     const BwdArgs a{dy, h, rstd, weight, dh, dscale ? r : nullptr, scale, dp, dx, dr, direct ? dweight : workspace, rows, D, grid};
     const cudaError_t e = stream_dt == GDN2_BF16 ? bwd_sized<bf16, bf16>(a, st)

@@ -99,7 +99,7 @@ gdn2_status check_norm(int rows, int D, double p, const void *rng, gdn2_dtype st
         return fail(GDN2_ERR_UNSUPPORTED, "%s", "unknown dtype");
     if (stream_dt == GDN2_BF16 && dt == GDN2_FP32)
         return fail(GDN2_ERR_UNSUPPORTED, "%s", "a BF16 residual stream with an FP32 branch");
-    if (D < 1 || D > 16384) return fail(GDN2_ERR_UNSUPPORTED, "%s", "D must be 1 to 16384");
+    if (D < 1 || D > 8192) return fail(GDN2_ERR_UNSUPPORTED, "%s", "D must be 1 to 8192");
     if (!(p >= 0.0 && p < 1.0)) return fail(GDN2_ERR_INVALID_ARG, "%s", "p must be in [0, 1)");
     if (p > 0.0 && !rng) return fail(GDN2_ERR_INVALID_ARG, "%s", "dropout needs rng");
     return GDN2_OK;
@@ -510,7 +510,7 @@ gdn2_status gdn2_residual_norm(const void *x, const void *r, const float *weight
 }
 
 size_t gdn2_residual_norm_bwd_workspace_size(int rows, int D) {
-    if (rows <= 0 || D < 1 || D > 16384) return 0;
+    if (rows <= 0 || D < 1 || D > 8192) return 0;
     return gdn2::residual_norm_bwd_workspace_bytes(rows, D);
 }
 

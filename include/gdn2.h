@@ -264,7 +264,7 @@ size_t gdn2_output_gate_bwd_workspace_size(int d_v);
  *   rstd       [rows]     float       written (for the gradient)
  *
  * Types: stream_dt, dt both BF16, both FP32, or an FP32 stream with a BF16 branch.
- * D from 1 to 16384 (multiples of 8 run vectorised).  rows = 0 is a no-op.
+ * D from 1 to 8192 (GDN2_ERR_UNSUPPORTED beyond).  rows = 0 is a no-op.
  */
 gdn2_status gdn2_residual_norm(const void *x, const void *r, const float *weight, const float *scale, double p,
                                const uint64_t *rng, float eps, void *h, void *y, float *rstd, int rows, int D,

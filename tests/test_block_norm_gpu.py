@@ -66,7 +66,7 @@ def check_backward(d, h, rstd, out, p, scale, branch=True, dh=True):
     dx = rs * (t - n * (t * n).mean(-1, keepdim=True)) + extra
     mag = rs * (t.abs() + n.abs() * (t * n).abs().mean(-1, keepdim=True)) + extra.abs()
     p64.assert_close("dx", out["dx"], dx, mag, 88)
-    depth = 8 + 32 + B * T / 148 + 148 * 16 / 32
+    depth = 8 + 32 + B * T / 144 + 148 * 16 / 32
     p64.assert_close("dweight", out["dweight"], (dy * n).sum((0, 1)), (dy * n).abs().sum((0, 1)), depth)
     if branch:
         f = kept * d["s"].double() if scale else kept
@@ -77,7 +77,8 @@ def check_backward(d, h, rstd, out, p, scale, branch=True, dh=True):
 
 
 SIZES = [(1, 1, 1), (1, 3, 7), (2, 5, 64), (1, 1, 2048), (3, 41, 1021), (1, 700, 512), (2, 150, 2048), (1, 33, 4104),
-         (1, 9, 8192), (1, 5, 8197), (2, 3, 16384), (1, 2, 16383), (1, 3000, 96)]
+         (1, 9, 8192), (1, 5, 8191), (1, 160, 8187), (1, 160, 8188), (1, 2, 6001), (1, 300, 4100), (1, 3000, 96), (1, 9000, 18),
+         (1, 5000, 45), (1, 1500, 515), (1, 1000, 1023)]
 
 
 @pytest.mark.parametrize("types", TYPES)

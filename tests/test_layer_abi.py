@@ -36,7 +36,7 @@ def test_residual_norm_refusals(lib):
     for name in ("x", "r", "weight", "scale", "rng", "h", "y", "rstd"):
         assert call(f, a, **{name: A * 20 + 4}) == INVALID and b"aligned" in lib.gdn2_last_error()
     assert call(f, a, rows=-1) == INVALID
-    assert call(f, a, D=0) == UNSUPPORTED and call(f, a, D=16385) == UNSUPPORTED
+    assert call(f, a, D=0) == UNSUPPORTED and call(f, a, D=8193) == UNSUPPORTED
     assert call(f, a, dt=7) == UNSUPPORTED and call(f, a, sdt=BF16, dt=FP32) == UNSUPPORTED
     for p in (-0.1, 1.0, 1.5, float("nan")):
         assert call(f, a, p=p) == INVALID
@@ -55,7 +55,7 @@ def test_residual_norm_bwd_refusals(lib):
     need = lib.gdn2_residual_norm_bwd_workspace_size(4, 128)
     assert need == 4 * 2 * 128 * 4                                           # a row of partial sums per CTA
     assert lib.gdn2_residual_norm_bwd_workspace_size(0, 128) == 0
-    assert lib.gdn2_residual_norm_bwd_workspace_size(4, 16385) == 0
+    assert lib.gdn2_residual_norm_bwd_workspace_size(4, 8193) == 0
     a = dict(dy=A, h=2 * A, rstd=3 * A, weight=4 * A, dh=5 * A, r=6 * A, scale=7 * A, p=0.1, rng=8 * A, dx=9 * A, dr=10 * A,
              dweight=11 * A, dscale=12 * A, ws=13 * A, ws_bytes=need, rows=4, D=128, sdt=BF16, dt=BF16, stream=None)
     for name in ("dy", "h", "rstd", "weight", "dx", "dweight", "ws"):
@@ -64,7 +64,7 @@ def test_residual_norm_bwd_refusals(lib):
         assert call(f, a, **{name: None}) == INVALID and b"dscale" in lib.gdn2_last_error()
     assert call(f, a, ws_bytes=need - 1) == INVALID and b"workspace" in lib.gdn2_last_error()
     assert call(f, a, rng=None) == INVALID and call(f, a, p=1.0) == INVALID and call(f, a, rows=-1) == INVALID
-    assert call(f, a, D=16385) == UNSUPPORTED and call(f, a, dt=FP32) == UNSUPPORTED
+    assert call(f, a, D=8193) == UNSUPPORTED and call(f, a, dt=FP32) == UNSUPPORTED
     for out, at in (("dx", A), ("dx", 2 * A), ("dr", A), ("dr", 9 * A), ("dweight", 4 * A), ("dscale", 11 * A), ("ws", 6 * A), ("dx", 5 * A + 16)):
         assert call(f, a, **{out: at}) == INVALID and b"overlaps" in lib.gdn2_last_error()
 
