@@ -178,6 +178,15 @@ def _need(t, name, dtype, shape, device):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+def _same(tensors, dtype, shape, index):
+    """Whether all tensors have this dtype and shape, on this device, contiguous: the checks of _need without a
+    call for each (0.15 us less a tensor).  Where they fail, _need says of which tensor and why."""
+    for t in tensors:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+            return False
+    return True
+
+
 def _stream(stream, device):
     if stream is not None:
         return stream.cuda_stream
@@ -594,9 +603,9 @@ def gdn2_output_gate_bwd(dy, o, g, weight, eps=1e-6, *, workspace=None, out=None
     B, T, H, dv = shape = dy.shape
     dev, dt = dy.device, dy.dtype
     code = _dtype_code(dy)
-    _need(dy, "dy", dt, shape, dev)
-    _need(o, "o", dt, shape, dev)
-    _need(g, "g", dt, shape, dev)
+    if not _same((dy, o, g), dt, shape, dev.index):
+        for n, t in (("dy", dy), ("o", o), ("g", g)):
+            _need(t, n, dt, shape, dev)
     _need(weight, "weight", torch.float32, (dv,), dev)
     out = out or {}
     grads = {}
@@ -624,12 +633,12 @@ def _slot_steps(name, gates, q, k, v, alpha, b, w, pool, slots, cu_seqlens, keep
     dv = v.shape[-1]
     dev, dt = q.device, q.dtype if gates is torch.float32 else torch.bfloat16
     code = _dtype_code(q)
-    _need(q, "q", dt, (T, H, dk), dev)
-    _need(k, "k", dt, (T, H, dk), dev)
-    _need(v, "v", dt, (T, H, dv), dev)
-    _need(alpha, "alpha", gates, (T, H, dk), dev)
-    _need(b, "b", gates, (T, H, dk), dev)
-    _need(w, "w", gates, (T, H, dv), dev)
+    key, value = (T, H, dk), (T, H, dv)
+    if not (_same((q, k), dt, key, dev.index) and _same((alpha, b), gates, key, dev.index)):
+        for n, t, d in (("q", q, dt), ("k", k, dt), ("alpha", alpha, gates), ("b", b, gates)):
+            _need(t, n, d, key, dev)
+    _need(v, "v", dt, value, dev)
+    _need(w, "w", gates, value, dev)
     if slots.dim() != 1:
         raise ValueError("slots: expected a 1-D tensor, one slot per sequence")
     N, n_slots = slots.shape[0], pool.shape[0]
@@ -644,12 +653,12 @@ def _slot_steps(name, gates, q, k, v, alpha, b, w, pool, slots, cu_seqlens, keep
     if (g is None) != (weight is None):
         raise ValueError("the epilogue needs both g and weight")
     if g is not None:
-        _need(g, "g", dt, (T, H, dv), dev)
+        _need(g, "g", dt, value, dev)
         _need(weight, "weight", torch.float32, (dv,), dev)
     if o is None:
-        o = _empty((T, H, dv), dt, q, stream)
+        o = _empty(value, dt, q, stream)
     else:
-        _need(o, "o", dt, (T, H, dv), dev)
+        _need(o, "o", dt, value, dev)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(b), _ptr(w), _ptr(pool), _ptr(slots), _ptr(cu_seqlens),
             _ptr(keep), _ptr(g), _ptr(weight), float(eps), _ptr(o), N, T, H, n_slots, dk, dv)
     with _on(dev):

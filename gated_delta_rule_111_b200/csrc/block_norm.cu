@@ -570,12 +570,6 @@ reduce_parts_kernel(const float *__restrict__ part, int G, int W, int D0, float 
     }
 }
 
-int device_sms() {
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-}
-
 // How a width is split over a CTA: 8 channels a thread up to 8,192; a few shifted widths
 // below that need one vector more.
 struct Split {
@@ -600,12 +594,6 @@ int grid_for(int rows, const Split &s, int per_sm, int sms) {
     return (int)(rows < cap ? rows : cap);
 }
 
-// More than 48 KB, static shared memory included, needs an opt-in.
-template <typename K> cudaError_t allow_smem(K kernel, size_t bytes) {
-    return bytes > 46 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
-                             : cudaSuccess;
-}
-
 struct FwdArgs {
     const void *x, *r;
     const float *weight, *scale;
@@ -622,9 +610,12 @@ cudaError_t fwd_launch(const FwdArgs &a, const Split &s, cudaStream_t st) {
     constexpr int S = 1;                     // 32 to 64 KB in flight an SM; two rows ahead measured slower
     auto kernel = residual_norm_kernel<TS, TB, SHIFT, VPT, MAXT, S>;
     const size_t smem = (size_t)MAXT * bytes * S;
-    const cudaError_t e = allow_smem(kernel, smem);
+    static std::atomic<unsigned long long> allowed{0};
+    int dev = 0, sms = 148;
+    cudaError_t e = device_sms(&dev, &sms);
+    if (e == cudaSuccess) e = allow_shared(kernel, (int)smem, dev, allowed);
     if (e != cudaSuccess) return e;
-    kernel<<<grid_for(a.rows, s, 1024, device_sms()), s.threads, smem, st>>>(
+    kernel<<<grid_for(a.rows, s, 1024, sms), s.threads, smem, st>>>(
         static_cast<const TS *>(a.x), static_cast<const TB *>(a.r), a.weight, a.scale, a.dp, a.eps,
         static_cast<TS *>(a.h), static_cast<TB *>(a.y), a.rstd, a.rows, a.D);
     return cudaGetLastError();
@@ -649,7 +640,10 @@ cudaError_t bwd_launch(const BwdArgs &a, const Split &s, cudaStream_t st) {
     auto kernel = residual_norm_bwd_kernel<TS, TB, SHIFT, VPT, MAXT, S>;
     constexpr bool shared_channels = MAXT > 512 && VPT * vector_channels<TS, TB>() == 8;     // weight and scale, see Channels
     const size_t smem = (size_t)MAXT * (bytes * S + (shared_channels ? 2 * 8 * 4 : 0));
-    const cudaError_t e = allow_smem(kernel, smem);
+    static std::atomic<unsigned long long> allowed{0};
+    int dev = 0, sms = 148;
+    cudaError_t e = device_sms(&dev, &sms);
+    if (e == cudaSuccess) e = allow_shared(kernel, (int)smem, dev, allowed);
     if (e != cudaSuccess) return e;
     kernel<<<a.grid, s.threads, smem, st>>>(
         static_cast<const TB *>(a.dy), static_cast<const TS *>(a.h), a.rstd, a.weight, static_cast<const TS *>(a.dh),

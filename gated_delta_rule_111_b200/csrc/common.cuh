@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "gdn2.h"
 
 namespace gdn2 {
@@ -26,6 +28,21 @@ __device__ __forceinline__ float clamp_alpha(float a) { return fmaxf(a, 1.175494
 // Streaming (read-once / write-once) 16-byte accesses for the decode state.
 __device__ __forceinline__ float4 ld_stream(const float4 *p) { return __ldcs(p); }
 __device__ __forceinline__ void st_stream(float4 *p, float4 v) { __stcs(p, v); }
+
+// The device's number of SMs, and a kernel's opt-in to more than 48 KB of shared memory,
+// asked for once per device (`done`: one bit a device, a static of the call's own).
+inline cudaError_t device_sms(int *dev, int *sms) {
+    cudaError_t e = cudaGetDevice(dev);
+    return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+}
+template <typename K>
+cudaError_t allow_shared(K kernel, int bytes, int dev, std::atomic<unsigned long long> &done) {
+    const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+    if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Host-side launchers (one per kernel family); each returns cudaGetLastError().
 cudaError_t launch_recurrent_step(const void *q, const void *k, const void *v, const float *alpha,

@@ -336,7 +336,7 @@ slot_steps_kernel(const __grid_constant__ StepArgs a) {
         if (planner) {
             plan.base = plan.t1 = plan.round = plan.sent = 0;
             plan.next_seq = item_of(a, order, 0, plan.next_head);
-            for (int n = 0; n < 3; ++n) plan_unit(a, order, plan, units[n], false);
+            plan_unit(a, order, plan, units[0], false);
         }
     }
     __syncthreads();
@@ -348,12 +348,16 @@ slot_steps_kernel(const __grid_constant__ StepArgs a) {
         copy_commit();
         fetch_state(u);
         copy_commit();
+        if (planner) {
+            plan_unit(a, order, plan, units[1], false);
+            plan_unit(a, order, plan, units[2], false);
+        }
         const bool clash = clashes(u);
         copy_wait<1>();
         prepare(u, 0);
+        dead = __syncthreads_or(clash);
         fetch_token(units[1]);
         copy_commit();
-        dead = __syncthreads_or(clash);
         if (dead && planner) atomicOr(&g_slot_conflict, 1u);
     }
 
@@ -499,11 +503,9 @@ slot_steps_kernel(const __grid_constant__ StepArgs a) {
 template <typename TIn, int DK, int DV, bool LOGITS> cudaError_t launch_typed(const StepArgs &a, cudaStream_t st) {
     using X = Shape<TIn, DK, DV, LOGITS>;
     int dev = 0, sms = 148;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(slot_steps_kernel<TIn, DK, DV, LOGITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 X::BYTES);
+    static std::atomic<unsigned long long> allowed{0};
+    cudaError_t e = device_sms(&dev, &sms);
+    if (e == cudaSuccess) e = allow_shared(slot_steps_kernel<TIn, DK, DV, LOGITS>, X::BYTES, dev, allowed);
     if (e != cudaSuccess) return e;
     const int items = a.N * a.H, cap = sms * X::CTAS;
     slot_steps_kernel<TIn, DK, DV, LOGITS><<<items < cap ? items : cap, X::THREADS, X::BYTES, st>>>(a);

@@ -157,8 +157,7 @@ int state_copy_max_pairs() { return kMaxPairs; }
 cudaError_t launch_state_copy(const float *src_pool, float *dst_pool, const int *src, const int *dst, int n,
                               int layers, int n_src, int n_dst, size_t state_floats, cudaStream_t st) {
     int dev = 0, sms = 148;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaError_t e = device_sms(&dev, &sms);
     if (e != cudaSuccess) return e;
     // One slice read ahead of the one that is written, unless the pairs are so many that half
     // the ring holds only 32 bytes (a sector) of each: then the whole ring is one slice.
@@ -174,7 +173,8 @@ cudaError_t launch_state_copy(const float *src_pool, float *dst_pool, const int 
                   "shared memory of a CTA");
     const size_t smem = ring_at * sizeof(int) + kRing * 16;
     auto kernel = ahead ? state_copy_kernel<2> : state_copy_kernel<1>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<unsigned long long> allowed[2];
+    e = allow_shared(kernel, 3 * kMaxPairs * (int)sizeof(int) + kRing * 16, dev, allowed[ahead]);
     if (e != cudaSuccess) return e;
     const long long items = (long long)layers * (long long)((state_floats / 4) >> log_w);
     kernel<<<(unsigned)(items < sms ? items : sms), kThreads, smem, st>>>(
