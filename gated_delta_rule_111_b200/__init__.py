@@ -158,7 +158,7 @@ _current = contextlib.nullcontext()
 
 def _on(device):
     """A context in which ``device`` is current; the one that is current already costs nothing to enter."""
-    return _current if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return _current if _current_device() == device.index else torch.cuda.device(device)
 
 
 def _need(t, name, dtype, shape, device):
@@ -176,15 +176,26 @@ def _need(t, name, dtype, shape, device):
 
 # The current stream's handle without a Stream object around it (2 us less a call), where torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _same(tensors, dtype, shape, index):
-    """Whether all tensors have this dtype and shape, on this device, contiguous: the checks of _need without a
-    call for each (0.15 us less a tensor).  Where they fail, _need says of which tensor and why."""
+def _same(index, dtype, shape, *tensors):
+    """Whether every tensor (None apart) has this dtype and shape, on this device, contiguous: the checks of
+    _need without a call for each.  Where they fail, _explain says of which tensor and why."""
     for t in tensors:
-        if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != index
+                              or not t.is_contiguous()):
             return False
     return True
+
+
+def _explain(device, *groups):
+    """Raises for the first tensor that is not as its group (dtype, shape, {name: tensor}) wants it."""
+    for dtype, shape, tensors in groups:
+        for name, t in tensors.items():
+            if t is not None:
+                _need(t, name, dtype, shape, device)
+    raise ValueError(f"arguments on different devices (expected {device})")
 
 
 def _stream(stream, device):
@@ -501,34 +512,27 @@ def gdn2_residual_norm(x, r, weight, eps=1e-6, *, scale=None, p=0.0, rng=None, h
     CUDA tensor (seed, offset).  Returns (h, y, rstd): h in x's dtype (x itself where r is None), y in
     r's (x's where r is None, unless ``y`` is given), rstd [B,T] fp32.  h may be x and y may be r (in place)."""
     lib = load_library()
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError("gdn2_residual_norm needs CUDA tensors (there is no CPU implementation)")
     shape, dev, sdt = x.shape, x.device, x.dtype
     rows, D = _rows(shape), shape[2]
-    dt = r.dtype if r is not None else y.dtype if y is not None else sdt
-    scode, code = _dtype_code(x), _dtype_code(r if r is not None else y if y is not None else x)
-    _need(x, "x", sdt, shape, dev)
-    _need(weight, "weight", torch.float32, (D,), dev)
-    if r is not None:
-        _need(r, "r", dt, shape, dev)
-    if scale is not None:
-        _need(scale, "scale", torch.float32, (D,), dev)
+    if r is None and h is not None:
+        raise ValueError("h: there is no addition to write without r")
+    like = r if r is not None else y if y is not None else x
+    dt = like.dtype
+    scode, code = _dtype_code(x), _dtype_code(like)
     p, rng = _dropout(p, rng, dev)
-    if r is None:
-        if h is not None:
-            raise ValueError("h: there is no addition to write without r")
-    elif h is None:
+    f32 = torch.float32
+    if not (_same(dev.index, sdt, shape, x, h) and _same(dev.index, dt, shape, r, y)
+            and _same(dev.index, f32, (D,), weight, scale) and _same(dev.index, f32, shape[:2], rstd)):
+        _explain(dev, (sdt, shape, {"x": x, "h": h}), (dt, shape, {"r": r, "y": y}),
+                 (f32, (D,), {"weight": weight, "scale": scale}), (f32, shape[:2], {"rstd": rstd}))
+    if h is None and r is not None:
         h = _empty(shape, sdt, x, stream)
-    else:
-        _need(h, "h", sdt, shape, dev)
     if y is None:
         y = _empty(shape, dt, x, stream)
-    else:
-        _need(y, "y", dt, shape, dev)
     if rstd is None:
-        rstd = _empty(shape[:2], torch.float32, x, stream)
-    else:
-        _need(rstd, "rstd", torch.float32, shape[:2], dev)
+        rstd = _empty(shape[:2], f32, x, stream)
     with _on(dev):
         _check(lib.gdn2_residual_norm(_ptr(x), _ptr(r), _ptr(weight), _ptr(scale), p, _ptr(rng), float(eps), _ptr(h),
                                       _ptr(y), _ptr(rstd), rows, D, scode, code, _stream(stream, dev)))
@@ -549,39 +553,40 @@ def gdn2_residual_norm_bwd(dy, h, rstd, weight, *, dh=None, r=None, scale=None, 
     scale).  ``out``: a dict of preallocated gradients (dx may be dh); ``workspace``: a uint8 CUDA tensor
     of at least gdn2_residual_norm_bwd_workspace_size bytes."""
     lib = load_library()
-    if dy.device.type != "cuda":
+    if not dy.is_cuda:
         raise ValueError("gdn2_residual_norm_bwd needs CUDA tensors (there is no CPU implementation)")
     shape, dev, dt, sdt = dy.shape, dy.device, dy.dtype, h.dtype
     rows, D = _rows(shape), shape[2]
     scode, code = _dtype_code(h), _dtype_code(dy)
-    _need(dy, "dy", dt, shape, dev)
-    _need(h, "h", sdt, shape, dev)
-    _need(rstd, "rstd", torch.float32, shape[:2], dev)
-    _need(weight, "weight", torch.float32, (D,), dev)
-    if dh is not None:
-        _need(dh, "dh", sdt, shape, dev)
     if not branch and (scale is not None or float(p) > 0.0):
         raise ValueError("scale and dropout belong to a branch")
-    if scale is not None:
-        _need(scale, "scale", torch.float32, (D,), dev)
-        if r is None:
-            raise ValueError("the gradient of scale needs r")
-        _need(r, "r", dt, shape, dev)
+    if scale is None:
+        r = None                                   # read for the gradient of scale alone
+    elif r is None:
+        raise ValueError("the gradient of scale needs r")
     p, rng = _dropout(p, rng, dev)
-    out = out or {}
-    g = {}
-    for name, want, s, d in (("dx", True, shape, sdt), ("dr", branch, shape, dt),
-                             ("dweight", True, (D,), torch.float32), ("dscale", scale is not None, (D,), torch.float32)):
-        t = out.get(name) if want else None
-        if t is not None:
-            _need(t, name, d, s, dev)
-        elif want:
-            t = _empty(s, d, dy, stream)
-        g[name] = t
+    get = (out or {}).get
+    g = {"dx": get("dx"), "dr": get("dr") if branch else None, "dweight": get("dweight"),
+         "dscale": get("dscale") if scale is not None else None}
+    f32 = torch.float32
+    if not (_same(dev.index, dt, shape, dy, r, g["dr"]) and _same(dev.index, sdt, shape, h, dh, g["dx"])
+            and _same(dev.index, f32, (D,), weight, scale, g["dweight"], g["dscale"])
+            and _same(dev.index, f32, shape[:2], rstd)):
+        _explain(dev, (dt, shape, {"dy": dy, "r": r, "dr": g["dr"]}), (sdt, shape, {"h": h, "dh": dh, "dx": g["dx"]}),
+                 (f32, (D,), {"weight": weight, "scale": scale, "dweight": g["dweight"], "dscale": g["dscale"]}),
+                 (f32, shape[:2], {"rstd": rstd}))
+    if g["dx"] is None:
+        g["dx"] = _empty(shape, sdt, dy, stream)
+    if branch and g["dr"] is None:
+        g["dr"] = _empty(shape, dt, dy, stream)
+    if g["dweight"] is None:
+        g["dweight"] = _empty((D,), f32, dy, stream)
+    if scale is not None and g["dscale"] is None:
+        g["dscale"] = _empty((D,), f32, dy, stream)
     with _on(dev):
         ws = _workspace(workspace, int(lib.gdn2_residual_norm_bwd_workspace_size(rows, D)), dy, stream)
         _check(lib.gdn2_residual_norm_bwd(_ptr(dy), _ptr(h), _ptr(rstd), _ptr(weight), _ptr(dh),
-                                          _ptr(r) if scale is not None else None, _ptr(scale), p, _ptr(rng),
+                                          _ptr(r), _ptr(scale), p, _ptr(rng),
                                           _ptr(g["dx"]), _ptr(g["dr"]), _ptr(g["dweight"]), _ptr(g["dscale"]),
                                           _ptr(ws), ws.numel() * ws.element_size(), rows, D, scode, code,
                                           _stream(stream, dev)))
@@ -598,24 +603,24 @@ def gdn2_output_gate_bwd(dy, o, g, weight, eps=1e-6, *, workspace=None, out=None
     Returns a dict with do, dg (dy's dtype) and dweight [dv] fp32.  ``out``: a dict of preallocated
     gradients; ``workspace``: a uint8 CUDA tensor of at least gdn2_output_gate_bwd_workspace_size bytes."""
     lib = load_library()
-    if dy.device.type != "cuda":
+    if not dy.is_cuda:
         raise ValueError("gdn2_output_gate_bwd needs CUDA tensors (there is no CPU implementation)")
     B, T, H, dv = shape = dy.shape
     dev, dt = dy.device, dy.dtype
     code = _dtype_code(dy)
-    if not _same((dy, o, g), dt, shape, dev.index):
-        for n, t in (("dy", dy), ("o", o), ("g", g)):
-            _need(t, n, dt, shape, dev)
-    _need(weight, "weight", torch.float32, (dv,), dev)
-    out = out or {}
-    grads = {}
-    for name, s, d in (("do", shape, dt), ("dg", shape, dt), ("dweight", (dv,), torch.float32)):
-        t = out.get(name)
-        if t is None:
-            t = _empty(s, d, dy, stream)
-        else:
-            _need(t, name, d, s, dev)
-        grads[name] = t
+    get = (out or {}).get
+    grads = {"do": get("do"), "dg": get("dg"), "dweight": get("dweight")}
+    f32 = torch.float32
+    if not (_same(dev.index, dt, shape, dy, o, g, grads["do"], grads["dg"])
+            and _same(dev.index, f32, (dv,), weight, grads["dweight"])):
+        _explain(dev, (dt, shape, {"dy": dy, "o": o, "g": g, "do": grads["do"], "dg": grads["dg"]}),
+                 (f32, (dv,), {"weight": weight, "dweight": grads["dweight"]}))
+    if grads["do"] is None:
+        grads["do"] = _empty(shape, dt, dy, stream)
+    if grads["dg"] is None:
+        grads["dg"] = _empty(shape, dt, dy, stream)
+    if grads["dweight"] is None:
+        grads["dweight"] = _empty((dv,), f32, dy, stream)
     with _on(dev):
         ws = _workspace(workspace, int(lib.gdn2_output_gate_bwd_workspace_size(dv)), dy, stream)
         _check(lib.gdn2_output_gate_bwd(_ptr(dy), _ptr(o), _ptr(g), _ptr(weight), float(eps), _ptr(grads["do"]),
@@ -627,38 +632,30 @@ def gdn2_output_gate_bwd(dy, o, g, weight, eps=1e-6, *, workspace=None, out=None
 def _slot_steps(name, gates, q, k, v, alpha, b, w, pool, slots, cu_seqlens, keep, g, weight, eps, o, stream):
     """Checks and the call of gdn2_slot_steps (gates fp32) and gdn2_slot_steps_logits (everything bf16)."""
     lib = load_library()
-    if q.device.type != "cuda":
+    if not q.is_cuda:
         raise ValueError(f"{name} needs CUDA tensors (there is no CPU implementation)")
     T, H, dk = q.shape
     dv = v.shape[-1]
-    dev, dt = q.device, q.dtype if gates is torch.float32 else torch.bfloat16
+    dev, f32, i32 = q.device, torch.float32, torch.int32
+    dt = q.dtype if gates is f32 else torch.bfloat16
     code = _dtype_code(q)
-    key, value = (T, H, dk), (T, H, dv)
-    if not (_same((q, k), dt, key, dev.index) and _same((alpha, b), gates, key, dev.index)):
-        for n, t, d in (("q", q, dt), ("k", k, dt), ("alpha", alpha, gates), ("b", b, gates)):
-            _need(t, n, d, key, dev)
-    _need(v, "v", dt, value, dev)
-    _need(w, "w", gates, value, dev)
     if slots.dim() != 1:
         raise ValueError("slots: expected a 1-D tensor, one slot per sequence")
     N, n_slots = slots.shape[0], pool.shape[0]
-    _need(pool, "pool", torch.float32, (n_slots, H, dk, dv), dev)
-    _need(slots, "slots", torch.int32, (N,), dev)
-    if cu_seqlens is not None:
-        _need(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
-    elif T != N:
+    if cu_seqlens is None and T != N:
         raise ValueError(f"{N} sequences with {T} tokens: without cu_seqlens every sequence has one token")
-    if keep is not None:
-        _need(keep, "keep", torch.int32, (N,), dev)
     if (g is None) != (weight is None):
         raise ValueError("the epilogue needs both g and weight")
-    if g is not None:
-        _need(g, "g", dt, value, dev)
-        _need(weight, "weight", torch.float32, (dv,), dev)
+    key, value, i = (T, H, dk), (T, H, dv), dev.index
+    if not (_same(i, dt, key, q, k) and _same(i, gates, key, alpha, b) and _same(i, dt, value, v, g, o)
+            and _same(i, gates, value, w) and _same(i, f32, (n_slots, H, dk, dv), pool) and _same(i, i32, (N,), slots, keep)
+            and _same(i, i32, (N + 1,), cu_seqlens) and _same(i, f32, (dv,), weight)):
+        _explain(dev, (dt, key, {"q": q, "k": k}), (gates, key, {"alpha": alpha, "b": b}),
+                 (dt, value, {"v": v, "g": g, "o": o}), (gates, value, {"w": w}),
+                 (f32, (n_slots, H, dk, dv), {"pool": pool}), (i32, (N,), {"slots": slots, "keep": keep}),
+                 (i32, (N + 1,), {"cu_seqlens": cu_seqlens}), (f32, (dv,), {"weight": weight}))
     if o is None:
         o = _empty(value, dt, q, stream)
-    else:
-        _need(o, "o", dt, value, dev)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(b), _ptr(w), _ptr(pool), _ptr(slots), _ptr(cu_seqlens),
             _ptr(keep), _ptr(g), _ptr(weight), float(eps), _ptr(o), N, T, H, n_slots, dk, dv)
     with _on(dev):
