@@ -332,7 +332,7 @@ residual_norm_kernel(const TS *x, const TB *r, const float *__restrict__ weight,
             rx.fetch(e_ahead, at);
             rr.fetch(e_ahead, at + RS::BYTES);
         }
-        ahead = ahead < rows ? ahead + grid : ahead;
+        ahead = ahead < rows - grid ? ahead + grid : rows;      // row + grid may pass 2^31
         e_ahead += step;
         copy_commit();
     };
@@ -390,7 +390,7 @@ residual_norm_kernel(const TS *x, const TB *r, const float *__restrict__ weight,
             store<TB, V, SHIFT>(y + e + (c - c0), c, D, hv[j]);
         }
         e += step;
-        if (row >= rows - grid) break;              // row + grid may pass 2^31
+        if (row >= rows - grid) break;
     }
 }
 
@@ -437,7 +437,7 @@ residual_norm_bwd_kernel(const TB *__restrict__ dy, const TS *__restrict__ h, co
             rdh.fetch(e_ahead, at + kDh);
             rr.fetch(e_ahead, at + kR);
         }
-        ahead = ahead < rows ? ahead + grid : ahead;
+        ahead = ahead < rows - grid ? ahead + grid : rows;      // row + grid may pass 2^31
         e_ahead += step;
         copy_commit();
     };
@@ -522,7 +522,7 @@ residual_norm_bwd_kernel(const TB *__restrict__ dy, const TS *__restrict__ h, co
             }
         }
         e += step;
-        if (last) break;                            // row + grid may pass 2^31
+        if (last) break;
     }
     float *pw = part + (size_t)blockIdx.x * (r ? 2 : 1) * D;
 #pragma unroll

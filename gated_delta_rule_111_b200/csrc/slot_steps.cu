@@ -43,7 +43,6 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr int kTile = 4;                  // tokens of a unit
 constexpr int kPlan = 8;                  // units in the plan's ring
-constexpr int kNear = 1;                  // slots of other sequences that a thread keeps in registers
 
 __device__ unsigned int g_slot_conflict = 0;   // nonzero: a slot was named by two sequences, one of them writing it
 
@@ -288,10 +287,11 @@ slot_steps_kernel(const __grid_constant__ StepArgs a) {
 #pragma unroll
         for (int e = 0; e < CV; ++e) z[lane * CV + e] = w[e] * v[e];
     };
-    // Two sequences that name one slot would race if either writes it: both are refused.
-    int near[kNear];
-#pragma unroll
-    for (int i = 0; i < kNear; ++i) near[i] = tid + i * THREADS < a.N ? __ldg(a.slots + tid + i * THREADS) : -1;
+    // Two sequences that name one slot would race if either writes it: both are refused.  Every
+    // item's slot is compared with all others', the first of them kept in a register, the rest
+    // read four at a time.
+    const int near = tid < a.N ? __ldg(a.slots + tid) : -1;
+    const bool by_four = (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0;
     auto clashes = [&](const Unit &u) {
         if (!u.first || u.count <= 0 || u.slot < 0 || u.slot >= a.n_slots) return false;
         bool clash = false;
@@ -300,9 +300,23 @@ slot_steps_kernel(const __grid_constant__ StepArgs a) {
             const Entry other = load_entry(a, m);
             clash |= other.t0 < other.t1 && (u.keep > 0 || other.keep > 0);
         };
-#pragma unroll
-        for (int i = 0; i < kNear; ++i) compare(tid + i * THREADS, near[i]);
-        for (int m = tid + kNear * THREADS; m < a.N; m += THREADS) compare(m, __ldg(a.slots + m));
+        compare(tid, near);
+        int done = THREADS;
+        if (by_four && a.N > THREADS) {
+            const int4 *four = reinterpret_cast<const int4 *>(a.slots);
+#pragma unroll 4
+            for (int m = THREADS / 4 + tid; m < a.N / 4; m += THREADS) {
+                const int4 v = __ldg(four + m);
+                if (v.x == u.slot || v.y == u.slot || v.z == u.slot || v.w == u.slot) {
+                    compare(4 * m, v.x);
+                    compare(4 * m + 1, v.y);
+                    compare(4 * m + 2, v.z);
+                    compare(4 * m + 3, v.w);
+                }
+            }
+            done = a.N / 4 * 4;
+        }
+        for (int m = done + tid; m < a.N; m += THREADS) compare(m, __ldg(a.slots + m));
         return clash;
     };
 

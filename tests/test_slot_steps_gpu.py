@@ -126,6 +126,27 @@ def test_shared_slots(g):
     assert g.gdn2_device_error() == 0
 
 
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("N", [130, 517, 1031])
+def test_shared_slots_among_many(g, N, shift):
+    """A slot named twice, at both ends and at every distance from a multiple of four, in an aligned slots tensor
+    and in one that is not."""
+    t, pool, _, _ = draw(N, 1, 64, 64, F32, False, N, seed=N)
+    buffer = torch.empty(N + 1, dtype=torch.int32, device="cuda")
+    slots = buffer[shift:N + shift]
+    for first, second in ((0, N - 1), (N - 2, N - 1), (1, 127), (2, N // 2), (N // 2 + 3, N - 3)):
+        slots.copy_(torch.arange(N, device="cuda"))
+        slots[second] = first
+        state = pool.clone()
+        o = g.gdn2_slot_steps(*t, state, slots)
+        assert g.gdn2_device_error() == 0x10000
+        dead = torch.zeros(N, dtype=torch.bool, device="cuda")
+        dead[[first, second]] = True
+        assert torch.equal((o == 0).all(-1).flatten(), dead)
+        assert torch.equal(state[first], pool[first]) and torch.equal(state[second], pool[second])
+        assert bool((state != pool).flatten(1).any(1)[~dead].all())
+
+
 def test_bad_offsets_stay_inside(g):
     """Offsets below zero, falling and past the end are clamped: no sequence reads or writes outside."""
     t, pool, _, _ = draw(6, 1, 64, 64, F32, False, 5, seed=9)
