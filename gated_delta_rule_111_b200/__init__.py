@@ -205,7 +205,8 @@ def _stream(stream, device):
 
 
 def gdn2_device_error(clear: bool = True) -> int:
-    """Synchronously read (and by default clear) the kernels' device-side failure flag."""
+    """Synchronously read (and by default clear) the kernels' device-side failure flag (0x10000: a slot-steps
+    call named one slot twice)."""
     lib = load_library()
     code = ctypes.c_uint(0)
     _check(lib.gdn2_device_error(ctypes.byref(code), int(clear)))

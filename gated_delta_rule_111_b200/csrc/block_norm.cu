@@ -23,9 +23,11 @@
 // masked when read and written element by element.
 //
 // Measured on a B200, 16,384 x 2,048, residual scale and p = 0.1: forward, BF16,
-// 49.0 us = 5.48 TB/s (45.7 us without dropout); FP32 stream and BF16 branch 63.9 us
-// = 6.30 TB/s; backward, FP32 stream, 94.3 us = 6.40 TB/s (99 % of a copy's rate), BF16
-// 73.8 us = 5.46 TB/s, bound there by the mask's and the conversions' instructions.
+// 49.5 us = 5.42 TB/s (45 us without dropout); FP32 stream and BF16 branch 64 us = 6.29
+// TB/s; backward, FP32 stream, 96.7 us = 6.25 TB/s (97 % of a copy's rate), BF16 74 us =
+// 5.45 TB/s, bound there by the mask's and the conversions' instructions.  Shifted rows:
+// 32,768 x 1,001 forward without dropout 49.5 us = 5.30 TB/s; 16,384 x 2,047 with it 89 us and
+// backward 240 us, because 257 vectors take a ninth warp.
 #include "async_copy.cuh"
 #include "common.cuh"
 #include "f32x2.cuh"

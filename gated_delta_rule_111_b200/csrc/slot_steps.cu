@@ -31,6 +31,12 @@
 // over the eight row groups by seven shuffles that halve the number of sums at each step.
 // Rows are paired in 64-bit registers for the packed FP32 multiply-adds of sm_100, which
 // halves their issue slots.
+//
+// Measured on a B200, 16 heads of 128 x 128, BF16: one token of 256 sequences 98 us = 5.57
+// TB/s (86 % of a copy's rate; 1,024 sequences 370 us = 5.92 TB/s), the same from logits with
+// the epilogue 97 us; a CTA per item, each load waiting for the one before, took 104 and
+// 125 us.  1 to 8 tokens of 48 sequences 28.5 us, 1 to 16 of 64 51 us: bound there by the
+// tokens' vectors from shared memory and the chain of shuffles, 16 warps an SM.
 #include <type_traits>
 
 #include "async_copy.cuh"
@@ -413,7 +419,7 @@ slot_steps_kernel(const __grid_constant__ StepArgs a) {
             const bool up = lane & 16, b3 = lane & 8, b2 = lane & 4;
             const int c_own = col + (b3 ? 2 : 0) + (b2 ? 1 : 0);
             const int last = units[n % kPlan].keep - 1;
-#pragma unroll 1                               // two tokens at once spill registers and cost a tenth
+#pragma unroll 1                               // unrolled, or two tokens to a pass over the state: spills, a tenth slower
             for (int i = 0; i < count; ++i) {
                 Pair r[4], p[4];
 #pragma unroll
