@@ -29,8 +29,8 @@
 // 32,768 x 1,001 forward without dropout 49.5 us = 5.30 TB/s; 16,384 x 2,047 with it 89 us and
 // backward 240 us, because 257 vectors take a ninth warp.
 #include "async_copy.cuh"
-#include "common.cuh"
 #include "f32x2.cuh"
+#include "layer.cuh"
 #include "philox.cuh"
 
 namespace gdn2 {

@@ -3,7 +3,7 @@
 #include <stdio.h>
 #include <string.h>
 
-#include "common.cuh"
+#include "layer.cuh"
 
 namespace gdn2 {
 void set_wait_limit(long long cycles);

@@ -14,7 +14,7 @@
 // Measured on a B200, 4 x 4,096 tokens x 16 heads of 128, BF16: 57.5 us = 5.83 TB/s (90 %
 // of a copy's rate) with three CTAs an SM; 71 us with four (the same kernel, more loads
 // in flight), 68 us with one row group at a time and five.
-#include "common.cuh"
+#include "layer.cuh"
 
 namespace gdn2 {
 namespace {

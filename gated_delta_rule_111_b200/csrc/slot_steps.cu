@@ -40,8 +40,8 @@
 #include <type_traits>
 
 #include "async_copy.cuh"
-#include "common.cuh"
 #include "f32x2.cuh"
+#include "layer.cuh"
 
 namespace gdn2 {
 namespace {

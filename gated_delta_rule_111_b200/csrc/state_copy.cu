@@ -22,7 +22,7 @@
 // 123 us = 6.14 TB/s (95 % of a copy's rate; 154 us with the slices held in registers
 // and nothing read ahead).
 #include "async_copy.cuh"
-#include "common.cuh"
+#include "layer.cuh"
 
 namespace gdn2 {
 namespace {
