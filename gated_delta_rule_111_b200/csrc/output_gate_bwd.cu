@@ -10,6 +10,8 @@
 // dweight adds up in registers over the rows of a lane, then over the CTA in shared
 // memory; each CTA writes one row of partial sums, and a second launch adds those in
 // a fixed order, so the result does not change from call to call.
+// 1 - s is formed by subtraction, so dg is right to 2^-24 of dy n weight where the gate
+// is nearly open, not to 2^-24 of itself; both sigmoids from exp(-|g|) took 63 us below.
 //
 // Measured on a B200, 4 x 4,096 tokens x 16 heads of 128, BF16: 57.5 us = 5.83 TB/s (90 %
 // of a copy's rate) with three CTAs an SM; 71 us with four (the same kernel, more loads

@@ -82,7 +82,7 @@ def test_training_step(g):
     Y2 = rms(H2) * leaves["w2"]
     ((dy.double() * Y2).sum() + (dh.double() * H2).sum()).backward()
 
-    assert float((y2.double() - Y2).norm() / Y2.norm()) < 1e-3
+    assert float((y2.double() - Y2.detach()).norm() / Y2.detach().norm()) < 1e-3
     got = dict(x=b1["dx"], r0=b1["dr"], w1=b1["dweight"], s1=b1["dscale"], w2=b2["dweight"], s2=b2["dscale"], wo=bg["dweight"])
     for name, t in got.items():
         ref = leaves[name].grad
