@@ -23,11 +23,12 @@
 // masked when read and written element by element.
 //
 // Measured on a B200, 16,384 x 2,048, residual scale and p = 0.1: forward, BF16,
-// 49.5 us = 5.42 TB/s (45 us without dropout); FP32 stream and BF16 branch 64 us = 6.29
-// TB/s; backward, FP32 stream, 96.7 us = 6.25 TB/s (97 % of a copy's rate), BF16 74 us =
-// 5.45 TB/s, bound there by the mask's and the conversions' instructions.  Shifted rows:
-// 32,768 x 1,001 forward without dropout 49.5 us = 5.30 TB/s; 16,384 x 2,047 with it 89 us and
-// backward 240 us, because 257 vectors take a ninth warp.
+// 49.8 us = 5.39 TB/s (45 us without dropout); FP32 stream and BF16 branch 66 us = 6.10
+// TB/s; backward, FP32 stream, 95.6 us = 6.32 TB/s (98 % of a copy's rate), BF16 74 us =
+// 5.45 TB/s, bound there by the mask's and the conversions' instructions.  6,553 x 5,120: 53,
+// 63, 100 and 78 us; 4,096 x 8,192: 53, 68, 116 and 99 us.  Shifted rows: 32,768 x 1,001
+// forward without dropout 49.5 us = 5.30 TB/s; 16,384 x 2,047 with it, BF16, 87 us and
+// backward 125 us, bound by putting the mask together and by the rows' ends.
 #include "async_copy.cuh"
 #include "f32x2.cuh"
 #include "layer.cuh"
@@ -151,18 +152,19 @@ template <typename T, int V, int VPT, int MAXT, int S, bool SHIFT> struct Rows {
     }
     // `e`: the element offset of the thread's first vector.  Past a row's end nothing is read (the last
     // row's may be the tensor's).
-    __device__ __forceinline__ void fetch(size_t e, uint32_t at) {
+    __device__ __forceinline__ void fetch(int j, size_t e, uint32_t at) {
         if (!base) return;
+        const int c = c0 + j * (int)blockDim.x * V;
+        const uint32_t to = at + threadIdx.x * B + j * MAXT * B;
+        if (c >= D) return;
+        if (SHIFT && c + V > D)
+            copy_async_part<B>(to, base + e + j * (int)blockDim.x * V, (D - c) * (int)sizeof(T));
+        else
+            copy_async<B>(to, base + e + j * (int)blockDim.x * V);
+    }
+    __device__ __forceinline__ void fetch(size_t e, uint32_t at) {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int c = c0 + j * (int)blockDim.x * V;
-            const uint32_t to = at + threadIdx.x * B + j * MAXT * B;
-            if (c >= D) continue;
-            if (SHIFT && c + V > D)
-                copy_async_part<B>(to, base + e + j * (int)blockDim.x * V, (D - c) * (int)sizeof(T));
-            else
-                copy_async<B>(to, base + e + j * (int)blockDim.x * V);
-        }
+        for (int j = 0; j < VPT; ++j) fetch(j, e, at);
     }
     __device__ __forceinline__ void read(int j, uint32_t at, Pair (&v)[V / 2], const uint32_t (*m)[V / 2] = nullptr) {
         RawOf<T, V> r;
@@ -224,9 +226,10 @@ template <int MAXT> __device__ __forceinline__ float cta_sum(float x, float *buf
     }
     if (lane == 0) buf[threadIdx.x >> 5] = x;
     __syncthreads();
-    x = (lane & (MAXT / 32 - 1)) < warps ? buf[lane & (MAXT / 32 - 1)] : 0.f;
+    constexpr int W = MAXT <= 64 ? 2 : MAXT <= 128 ? 4 : MAXT <= 256 ? 8 : MAXT <= 512 ? 16 : 32;
+    x = (lane & (W - 1)) < warps ? buf[lane & (W - 1)] : 0.f;
 #pragma unroll
-    for (int m = MAXT / 64; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    for (int m = W / 2; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
     return x;
 }
 
@@ -402,8 +405,15 @@ residual_norm_kernel(const TS *x, const TB *r, const float *__restrict__ weight,
 // A CTA adds its rows' shares of the two sums in registers and writes them to its
 // row of `part` ([gridDim][1 or 2][D]); reduce_parts_kernel adds those in a fixed
 // order, so the result does not change from call to call.
+// CTAs of the backward on an SM: 512 threads of 128 registers, or, where that would leave much
+// of the SM idle, three CTAs of 192 (112 registers) or two of 320 (96): 13,107 x 2,560 BF16 74
+// us, 96 with one CTA.  One CTA of more than 512 threads has 96 registers at 640, 80 at 768.
+constexpr int bwd_ctas(int maxt) { return maxt == 192 ? 3 : maxt == 320 ? 2 : maxt <= 512 ? 512 / maxt : 1; }
+// Those with fewer than 128 registers, and 16 channels a thread, keep weight and scale in shared memory.
+constexpr bool bwd_shared(int maxt, int channels) { return channels == 16 || maxt > 512 || maxt == 192 || maxt == 320; }
+
 template <typename TS, typename TB, bool SHIFT, int VPT, int MAXT, int S>
-__global__ void __launch_bounds__(MAXT, MAXT <= 512 ? 512 / MAXT : 1)
+__global__ void __launch_bounds__(MAXT, bwd_ctas(MAXT))
 residual_norm_bwd_kernel(const TB *__restrict__ dy, const TS *__restrict__ h, const float *__restrict__ rstd,
                          const float *__restrict__ weight, const TS *dh, const TB *__restrict__ r,
                          const float *__restrict__ scale, Dropout dp, TS *dx, TB *__restrict__ dr,
@@ -411,7 +421,9 @@ residual_norm_bwd_kernel(const TB *__restrict__ dy, const TS *__restrict__ h, co
     constexpr int V = vector_channels<TS, TB>(), P = V / 2;
     using RS = Rows<TS, V, VPT, MAXT, S, SHIFT>;
     using RB = Rows<TB, V, VPT, MAXT, S, SHIFT>;
-    using C = Channels<V, VPT, MAXT, (MAXT > 512 && VPT * V == 8)>;
+    using C = Channels<V, VPT, MAXT, bwd_shared(MAXT, VPT * V)>;
+    constexpr bool SPLIT = S == 1, DEEP = VPT * V == 16;       // DEEP: part of a row by part, to save registers
+    static_assert(SPLIT || !DEEP, "one stage");
     constexpr uint32_t kDh = RS::BYTES, kDy = 2 * RS::BYTES, kR = kDy + RB::BYTES, kStage = kR + RB::BYTES;
     extern __shared__ uint4 ring[];
     __shared__ float red[2][32];
@@ -432,19 +444,33 @@ residual_norm_bwd_kernel(const TB *__restrict__ dy, const TS *__restrict__ h, co
     const size_t step = (size_t)grid * D;
     int row = blockIdx.x, ahead = row;                  // the row in hand and the next one to fetch
     size_t e = (size_t)row * D + c0, e_ahead = e;
-    auto fetch = [&](uint32_t at) {
-        if (ahead < rows) {
-            rdy.fetch(e_ahead, at + kDy);
-            rh.fetch(e_ahead, at);
-            rdh.fetch(e_ahead, at + kDh);
-            rr.fetch(e_ahead, at + kR);
-        }
+    // A row comes in two parts: what its sum is made of, and what is wanted after the sum.  With one
+    // row ahead (SPLIT) each part of the next row is sent for when this row's has been read (16,384 x
+    // 2,048 FP32 120 us against 128); with two, both after the sum (BF16 74 us against 96).
+    auto fetch_first = [&](int j, uint32_t at) {
+        if (ahead >= rows) return;
+        rdy.fetch(j, e_ahead, at + kDy);
+        rh.fetch(j, e_ahead, at);
+    };
+    auto fetch_rest = [&](int j, uint32_t at) {
+        if (ahead >= rows) return;
+        rdh.fetch(j, e_ahead, at + kDh);
+        rr.fetch(j, e_ahead, at + kR);
+    };
+    auto next_row = [&]() {
         ahead = ahead < rows - grid ? ahead + grid : rows;      // row + grid may pass 2^31
         e_ahead += step;
         copy_commit();
     };
 #pragma unroll
-    for (int i = 0; i < S; ++i) fetch(ring0 + i * kStage);
+    for (int i = 0; i < S; ++i) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) fetch_first(j, ring0 + i * kStage);
+        if (SPLIT) copy_commit();
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) fetch_rest(j, ring0 + i * kStage);
+        next_row();
+    }
     float rs_next = __ldg(rstd + row);
     C wt, sc;
     wt.init(weight, ring0 + S * kStage, c0, D, 0.f, 1.f);
@@ -472,12 +498,13 @@ residual_norm_bwd_kernel(const TB *__restrict__ dy, const TS *__restrict__ h, co
         }
         const float rs = rs_next;
         const Pair rs2 = pack2(rs, rs);
-        copy_wait<S - 1>();
-        Pair n[VPT][P], t[VPT][P], gx[VPT][P], b[VPT][P], dot2 = pack2(0.f, 0.f);
+        copy_wait<SPLIT ? 2 * S - 1 : S - 1>();
+        Pair n[VPT][P], t[VPT][P], dot2 = pack2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             rdy.read(j, at + kDy, t[j]);
             rh.read(j, at, n[j]);
+            if (DEEP) fetch_first(j, at);
             Pair w[P];
             wt.get(j, w);
 #pragma unroll
@@ -488,6 +515,10 @@ residual_norm_bwd_kernel(const TB *__restrict__ dy, const TS *__restrict__ h, co
                 dot2 = fma2(t[j][i], n[j][i], dot2);
             }
         }
+        if (SPLIT && !DEEP)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) fetch_first(j, at);
+        if (SPLIT) copy_commit();
         const bool last = row >= rows - grid;
         if (!last) rs_next = __ldg(rstd + row + grid);
         if (SHIFT && dp.rng && !last) keep.start(dp, key, offset, row + grid, left[it ^ 1]);
@@ -495,34 +526,47 @@ residual_norm_bwd_kernel(const TB *__restrict__ dy, const TS *__restrict__ h, co
         unpack2(dot2, d0, d1);
         const float mean = -cta_sum<MAXT>(d0 + d1, red[it]) * inv_d;
         const Pair mean2 = pack2(mean, mean);
+        if (SPLIT) copy_wait<2 * S - 1>();
+        constexpr int STEP = DEEP ? 1 : VPT;        // vectors whose part behind the sum is in registers at once
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            if (dh) rdh.read(j, at + kDh, gx[j]);
-            if (r) rr.read(j, at + kR, b[j], &keep.m[j]);
+        for (int j0 = 0; j0 < VPT; j0 += STEP) {
+            Pair gx[STEP][P], b[STEP][P];
 #pragma unroll
-            for (int i = 0; i < P; ++i)
-                if (!dh) gx[j][i] = pack2(0.f, 0.f);
+            for (int j = j0; j < j0 + STEP; ++j) {
+                if (dh) rdh.read(j, at + kDh, gx[j - j0]);
+                if (r) rr.read(j, at + kR, b[j - j0], &keep.m[j]);
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    if (!dh) gx[j - j0][i] = pack2(0.f, 0.f);
+            }
+#pragma unroll
+            for (int j = j0; j < j0 + STEP; ++j) {
+                if (!SPLIT) fetch_first(j, at);
+                fetch_rest(j, at);
+            }
+            if (!DEEP) next_row();
+#pragma unroll
+            for (int j = j0; j < j0 + STEP; ++j) {
+                const int c = c0 + j * (int)blockDim.x * V;
+                Pair (&d)[P] = gx[j - j0];
+#pragma unroll
+                for (int i = 0; i < P; ++i) d[i] = fma2(rs2, fma2(n[j][i], mean2, t[j][i]), d[i]);
+                store<TS, V, SHIFT>(dx + e + (c - c0), c, D, d);
+                if (r) {                            // as is scaled by 1 / (1 - p) at the end
+#pragma unroll
+                    for (int i = 0; i < P; ++i) as[j][i] = fma2(d[i], b[j - j0][i], as[j][i]);
+                }
+                if (dr) {
+                    Pair s[P];
+                    sc.get(j, s);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) d[i] = mul2(d[i], s[i]);
+                    store<TB, V, SHIFT>(dr + e + (c - c0), c, D, d, &keep.m[j]);
+                }
+            }
         }
-        fetch(at);                                  // this thread's part of the stage has been read
+        if (DEEP) next_row();
         at = at == ring0 + (S - 1) * kStage ? ring0 : at + kStage;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int c = c0 + j * (int)blockDim.x * V;
-#pragma unroll
-            for (int i = 0; i < P; ++i) gx[j][i] = fma2(rs2, fma2(n[j][i], mean2, t[j][i]), gx[j][i]);
-            store<TS, V, SHIFT>(dx + e + (c - c0), c, D, gx[j]);
-            if (r) {                                // as is scaled by 1 / (1 - p) at the end
-#pragma unroll
-                for (int i = 0; i < P; ++i) as[j][i] = fma2(gx[j][i], b[j][i], as[j][i]);
-            }
-            if (dr) {
-                Pair s[P];
-                sc.get(j, s);
-#pragma unroll
-                for (int i = 0; i < P; ++i) gx[j][i] = mul2(gx[j][i], s[i]);
-                store<TB, V, SHIFT>(dr + e + (c - c0), c, D, gx[j], &keep.m[j]);
-            }
-        }
         e += step;
         if (last) break;
     }
@@ -573,21 +617,25 @@ reduce_parts_kernel(const float *__restrict__ part, int G, int W, int D0, float 
 }
 
 // How a width is split over a CTA: 8 channels a thread up to 8,192; a few shifted widths
-// below that need one vector more.
+// below that need one vector more.  The backward gives a thread 16 channels above 6,144
+// (`deep`), where 8 would leave its threads 64 registers (4,096 x 8,192, FP32 stream: 115 us
+// against 125; at 5,120 the other way round, 100 against 144).
 struct Split {
     int threads;
-    bool shift, more;
+    bool shift, more, deep;
 };
-Split split_for(int D, int V) {
-    Split s{0, D % V != 0, false};
+Split split_for(int D, int V, bool bwd) {
+    Split s{0, D % V != 0, false, false};
     const int vectors = s.shift ? (D + 2 * V - 2) / V : D / V, k = 8 / V;
-    s.more = vectors > 1024 * k;
-    s.threads = s.more ? 1024 : ((vectors + k - 1) / k + 31) / 32 * 32;
+    s.deep = bwd && vectors > 768 * k;
+    s.more = !s.deep && vectors > 1024 * k;
+    const int each = s.deep ? 2 * k : s.more ? k + 1 : k;
+    s.threads = s.more ? 1024 : ((vectors + each - 1) / each + 31) / 32 * 32;
     return s;
 }
 
-// CTAs: as many as an SM holds (`per_sm` threads: 1,024 of the forward, 64 registers each, or 512
-// of the backward, whose two sums' accumulators take 128).  Shifted rows want a multiple of
+// CTAs: as many as an SM holds (`per_sm` threads: 1,024 of the forward, 64 registers each; of the
+// backward, whose two sums' accumulators take more, see bwd_ctas).  Shifted rows want a multiple of
 // 8 where a CTA gets several, so that they all start at the same place of a vector.
 int grid_for(int rows, const Split &s, int per_sm, int sms) {
     const int ctas = s.threads >= per_sm ? 1 : per_sm / s.threads;
@@ -609,7 +657,10 @@ struct FwdArgs {
 template <typename TS, typename TB, bool SHIFT, int VPT, int MAXT>
 cudaError_t fwd_launch(const FwdArgs &a, const Split &s, cudaStream_t st) {
     constexpr int bytes = VPT * vector_channels<TS, TB>() * (int)(sizeof(TS) + sizeof(TB));
-    constexpr int S = 1;                     // 32 to 64 KB in flight an SM; two rows ahead measured slower
+    // 32 to 64 KB in flight an SM: one row ahead where CTAs of 1,024 threads in all share it (two
+    // measured slower), two where one CTA of 513 to 768 has it alone and they are at most 72 KB
+    // (6,553 x 5,120, FP32 stream and BF16 branch: 63 us against 74; both FP32: 96 against 86).
+    constexpr int S = MAXT > 512 && MAXT <= 768 && 2 * bytes * MAXT <= 73728 ? 2 : 1;
     auto kernel = residual_norm_kernel<TS, TB, SHIFT, VPT, MAXT, S>;
     const size_t smem = (size_t)MAXT * bytes * S;
     static std::atomic<unsigned long long> allowed{0};
@@ -640,8 +691,8 @@ cudaError_t bwd_launch(const BwdArgs &a, const Split &s, cudaStream_t st) {
     // Two rows in flight where that is at most 96 KB an SM, else one: more measured slower.
     constexpr int S = 2 * bytes * (MAXT > 512 ? MAXT : 512) <= 98304 ? 2 : 1;
     auto kernel = residual_norm_bwd_kernel<TS, TB, SHIFT, VPT, MAXT, S>;
-    constexpr bool shared_channels = MAXT > 512 && VPT * vector_channels<TS, TB>() == 8;     // weight and scale, see Channels
-    const size_t smem = (size_t)MAXT * (bytes * S + (shared_channels ? 2 * 8 * 4 : 0));
+    constexpr bool shared_channels = bwd_shared(MAXT, VPT * vector_channels<TS, TB>());     // weight and scale, see Channels
+    const size_t smem = (size_t)MAXT * (bytes * S + (shared_channels ? 2 * VPT * vector_channels<TS, TB>() * 4 : 0));
     static std::atomic<unsigned long long> allowed{0};
     int dev = 0, sms = 148;
     cudaError_t e = device_sms(&dev, &sms);
@@ -654,34 +705,47 @@ cudaError_t bwd_launch(const BwdArgs &a, const Split &s, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-// The instance of LAUNCH (fwd_launch, bwd_launch) that a width needs; k vectors make 8 channels.
+// The instance that a width needs; k vectors make 8 channels.
 #define GDN2_BY_THREADS(LAUNCH, SHIFT)                                                         \
     {                                                                                          \
-        if (s.threads <= 64) return LAUNCH<TS, TB, SHIFT, k, 64>(a, s, st);            \
-        if (s.threads <= 128) return LAUNCH<TS, TB, SHIFT, k, 128>(a, s, st);          \
-        if (s.threads <= 256) return LAUNCH<TS, TB, SHIFT, k, 256>(a, s, st);          \
-        if (s.threads <= 512) return LAUNCH<TS, TB, SHIFT, k, 512>(a, s, st);          \
-        return LAUNCH<TS, TB, SHIFT, k, 1024>(a, s, st);                               \
+        if (s.threads <= 64) return LAUNCH<TS, TB, SHIFT, k, 64>(a, s, st);                    \
+        if (s.threads <= 128) return LAUNCH<TS, TB, SHIFT, k, 128>(a, s, st);                  \
+        if (s.threads <= 192) return LAUNCH<TS, TB, SHIFT, k, 192>(a, s, st);                  \
+        if (s.threads <= 256) return LAUNCH<TS, TB, SHIFT, k, 256>(a, s, st);                  \
+        if (s.threads <= 320) return LAUNCH<TS, TB, SHIFT, k, 320>(a, s, st);                  \
+        if (s.threads <= 512) return LAUNCH<TS, TB, SHIFT, k, 512>(a, s, st);                  \
+        if (s.threads <= 640) return LAUNCH<TS, TB, SHIFT, k, 640>(a, s, st);                  \
+        return LAUNCH<TS, TB, SHIFT, k, 768>(a, s, st);                                        \
     }
-#define GDN2_BY_WIDTH(LAUNCH)                                                                  \
-    constexpr int V = vector_channels<TS, TB>(), k = 8 / V;                                    \
-    const Split s = split_for(a.D, V);                                                         \
-    if (s.more) return LAUNCH<TS, TB, true, k + 1, 1024>(a, s, st);                    \
-    if (s.shift) GDN2_BY_THREADS(LAUNCH, true)                                                 \
-    GDN2_BY_THREADS(LAUNCH, false)
 
 template <typename TS, typename TB> cudaError_t fwd_sized(const FwdArgs &a, cudaStream_t st) {
-    GDN2_BY_WIDTH(fwd_launch)
+    constexpr int V = vector_channels<TS, TB>(), k = 8 / V;
+    const Split s = split_for(a.D, V, false);
+    if (s.more) return fwd_launch<TS, TB, true, k + 1, 1024>(a, s, st);
+    if (s.threads > 768)
+        return s.shift ? fwd_launch<TS, TB, true, k, 1024>(a, s, st) : fwd_launch<TS, TB, false, k, 1024>(a, s, st);
+    if (s.shift) GDN2_BY_THREADS(fwd_launch, true)
+    GDN2_BY_THREADS(fwd_launch, false)
 }
 template <typename TS, typename TB> cudaError_t bwd_sized(const BwdArgs &a, cudaStream_t st) {
-    GDN2_BY_WIDTH(bwd_launch)
+    constexpr int V = vector_channels<TS, TB>(), k = 8 / V;
+    const Split s = split_for(a.D, V, true);
+    if (s.deep) {
+        if (s.threads > 512) return bwd_launch<TS, TB, true, 2 * k, 544>(a, s, st);
+        return s.shift ? bwd_launch<TS, TB, true, 2 * k, 512>(a, s, st) : bwd_launch<TS, TB, false, 2 * k, 512>(a, s, st);
+    }
+    if (s.shift) GDN2_BY_THREADS(bwd_launch, true)
+    GDN2_BY_THREADS(bwd_launch, false)
 }
-#undef GDN2_BY_WIDTH
 #undef GDN2_BY_THREADS
 
 // CTAs of the backward: the workspace holds one row of partial sums for each, so
 // the count goes by the sizes alone (148 SMs).
-int bwd_grid(int rows, int D, int V) { return grid_for(rows, split_for(D, V), 512, 148); }
+int bwd_grid(int rows, int D, int V) {
+    const Split s = split_for(D, V, true);
+    const int tier = s.threads > 256 && s.threads <= 320 ? 320 : s.threads > 128 && s.threads <= 192 ? 192 : 512;
+    return grid_for(rows, s, tier * bwd_ctas(tier), 148);
+}
 int vector_of(gdn2_dtype stream_dt, gdn2_dtype dt) {
     return stream_dt == GDN2_BF16 ? vector_channels<bf16, bf16>()
            : dt == GDN2_BF16      ? vector_channels<float, bf16>()

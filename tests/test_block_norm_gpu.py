@@ -78,7 +78,8 @@ def check_backward(d, h, rstd, out, p, scale, branch=True, dh=True):
 
 SIZES = [(1, 1, 1), (1, 3, 7), (2, 5, 64), (1, 1, 2048), (3, 41, 1021), (1, 700, 512), (2, 150, 2048), (1, 33, 4104),
          (1, 9, 8192), (1, 5, 8191), (1, 160, 8187), (1, 160, 8188), (1, 2, 6001), (1, 300, 4100), (1, 3000, 96), (1, 9000, 18),
-         (1, 5000, 45), (1, 1500, 515), (1, 1000, 1023)]
+         (1, 5000, 45), (1, 1500, 515), (1, 1000, 1023), (1, 1000, 1448), (1, 1000, 1501), (1, 700, 2304), (1, 700, 2551),
+         (1, 500, 5120), (1, 500, 5113), (1, 450, 6144), (1, 450, 6139), (1, 320, 7168), (1, 320, 7003), (1, 320, 8192)]
 
 
 @pytest.mark.parametrize("types", TYPES)
