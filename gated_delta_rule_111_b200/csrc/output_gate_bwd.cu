@@ -108,7 +108,8 @@ output_gate_bwd_kernel(const T *__restrict__ dy, const T *__restrict__ o, const 
                 ss += __shfl_xor_sync(0xffffffffu, ss, m);
                 dot += __shfl_xor_sync(0xffffffffu, dot, m);
             }
-            const float rstd = rsqrtf(ss * (1.f / DV) + eps), mean = dot * rstd * (1.f / DV);
+            // behind the last row 0, so that without an eps its zeros add no 0 * inf to dweight
+            const float rstd = row < rows ? rsqrtf(ss * (1.f / DV) + eps) : 0.f, mean = dot * rstd * (1.f / DV);
             float x[N], y[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) {
