@@ -6,15 +6,16 @@
 //
 // Memory-bound: the forward reads x and r once and writes h and y once, the
 // backward reads dy, h, dh (and r for the scale's gradient) and writes dx and dr.
-// One CTA holds one row at a time, 8 channels a thread, and walks the rows with a
-// stride of the grid, so that weight and scale are read once per CTA and, in the
-// backward, their gradients accumulate in registers over the CTA's rows.  The next
-// rows arrive by asynchronous copies into shared memory.  What the layout has to
-// keep: a lane's access covers whole 32-byte sectors together with its neighbours'
-// (8 consecutive FP32 channels a lane cost 125 us where 4 cost 95, 16,384 x 2,048
-// backward with an FP32 stream), and only 32 to 96 KB an SM are in flight (deeper
-// rings were 5 to 15 % slower).  The dropout's integer work (about 80 instructions
-// per 8 channels) comes before the wait for a row's data.
+// One CTA holds one row at a time, 8 channels a thread (16 in the backward above
+// 6,144), and walks the rows with a stride of the grid, so that weight and scale are
+// read once per CTA and, in the backward, their gradients accumulate in registers over
+// the CTA's rows. The next rows arrive by asynchronous copies into shared memory. What
+// the layout has to keep: a lane's access covers whole 32-byte sectors together with
+// its neighbours' (8 consecutive FP32 channels a lane cost 125 us where 4 cost 95,
+// 16,384 x 2,048 backward with an FP32 stream), and not too much is in flight, 32 to
+// 96 KB an SM in the forward and 60 to 136 in the backward (deeper rings were 5 to 15
+// % slower). The dropout's integer work (about 80 instructions per 8 channels) comes
+// before the wait for a row's data.
 //
 // Where D is no multiple of a vector, rows start inside one.  A CTA's rows all start at
 // the same place of a vector, because they are a multiple of 8 rows apart, so its threads
@@ -180,8 +181,8 @@ template <typename T, int V, int VPT, int MAXT, int S, bool SHIFT> struct Rows {
 };
 
 // A [D] vector's channels of one thread, times `factor`; `fill` where p is null.  In
-// registers, or (SHARED: CTAs of 1,024 threads, which have 64 registers each) in the
-// thread's own part of shared memory.
+// registers, or (SHARED: instances of the backward that are short of them, bwd_shared) in
+// the thread's own part of shared memory.
 template <int V, int VPT, int MAXT, bool SHARED> struct Channels {
     Pair reg[SHARED ? 1 : VPT][V / 2];
     uint32_t at;
@@ -657,9 +658,9 @@ struct FwdArgs {
 template <typename TS, typename TB, bool SHIFT, int VPT, int MAXT>
 cudaError_t fwd_launch(const FwdArgs &a, const Split &s, cudaStream_t st) {
     constexpr int bytes = VPT * vector_channels<TS, TB>() * (int)(sizeof(TS) + sizeof(TB));
-    // 32 to 64 KB in flight an SM: one row ahead where CTAs of 1,024 threads in all share it (two
-    // measured slower), two where one CTA of 513 to 768 has it alone and they are at most 72 KB
-    // (6,553 x 5,120, FP32 stream and BF16 branch: 63 us against 74; both FP32: 96 against 86).
+    // One row ahead where CTAs of 1,024 threads in all share an SM, 32 to 64 KB (96 with a vector
+    // more; two rows measured slower), two where one CTA of 513 to 768 has it alone and they are at
+    // most 72 KB (6,553 x 5,120, FP32 stream and BF16 branch: 63 us against 74; both FP32: 96 against 86).
     constexpr int S = MAXT > 512 && MAXT <= 768 && 2 * bytes * MAXT <= 73728 ? 2 : 1;
     auto kernel = residual_norm_kernel<TS, TB, SHIFT, VPT, MAXT, S>;
     const size_t smem = (size_t)MAXT * bytes * S;
@@ -688,7 +689,10 @@ struct BwdArgs {
 template <typename TS, typename TB, bool SHIFT, int VPT, int MAXT>
 cudaError_t bwd_launch(const BwdArgs &a, const Split &s, cudaStream_t st) {
     constexpr int bytes = VPT * vector_channels<TS, TB>() * 2 * (int)(sizeof(TS) + sizeof(TB));
-    // Two rows in flight where that is at most 96 KB an SM, else one: more measured slower.
+    // Two rows in flight where 512 threads, or the CTA's if more, have at most 96 KB of them, else one.
+    // The three CTAs of 192 and the two of 320 then have 108 and 120 KB an SM with an FP32 stream and a
+    // BF16 branch, where one row is slower (23,172 x 1,448 100.4 us against 97.4, 13,107 x 2,560 97.1
+    // against 94.7).
     constexpr int S = 2 * bytes * (MAXT > 512 ? MAXT : 512) <= 98304 ? 2 : 1;
     auto kernel = residual_norm_bwd_kernel<TS, TB, SHIFT, VPT, MAXT, S>;
     constexpr bool shared_channels = bwd_shared(MAXT, VPT * vector_channels<TS, TB>());     // weight and scale, see Channels
