@@ -709,17 +709,32 @@ cudaError_t bwd_launch(const BwdArgs &a, const Split &s, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-// The instance that a width needs; k vectors make 8 channels.
-#define GDN2_BY_THREADS(LAUNCH, SHIFT)                                                         \
-    {                                                                                          \
-        if (s.threads <= 64) return LAUNCH<TS, TB, SHIFT, k, 64>(a, s, st);                    \
-        if (s.threads <= 128) return LAUNCH<TS, TB, SHIFT, k, 128>(a, s, st);                  \
-        if (s.threads <= 192) return LAUNCH<TS, TB, SHIFT, k, 192>(a, s, st);                  \
-        if (s.threads <= 256) return LAUNCH<TS, TB, SHIFT, k, 256>(a, s, st);                  \
-        if (s.threads <= 320) return LAUNCH<TS, TB, SHIFT, k, 320>(a, s, st);                  \
-        if (s.threads <= 512) return LAUNCH<TS, TB, SHIFT, k, 512>(a, s, st);                  \
-        if (s.threads <= 640) return LAUNCH<TS, TB, SHIFT, k, 640>(a, s, st);                  \
-        return LAUNCH<TS, TB, SHIFT, k, 768>(a, s, st);                                        \
+// The instance that a width needs; k vectors make 8 channels.  The forward's have 64 registers a thread
+// up to 512 threads and differ there in a stage's stride and the length of the last sum.  That matters
+// for CTAs of 32 threads, of which an SM holds 32 if their stages are short (131,072 x 256 BF16 49 us, 61
+// with the instance of 256); instances of 128, 192 and 320 measured like those of 256 and 512.  One of 640
+// may use more registers than one of 768 (6,553 x 5,120, FP32 stream, BF16 branch: 63 us against 67).  For
+// the backward's see bwd_ctas.
+#define GDN2_UP_TO(THREADS, LAUNCH, SHIFT) \
+    if (s.threads <= THREADS) return LAUNCH<TS, TB, SHIFT, k, THREADS>(a, s, st)
+#define GDN2_FWD(SHIFT)                                         \
+    {                                                           \
+        GDN2_UP_TO(64, fwd_launch, SHIFT);                      \
+        GDN2_UP_TO(256, fwd_launch, SHIFT);                     \
+        GDN2_UP_TO(512, fwd_launch, SHIFT);                     \
+        GDN2_UP_TO(640, fwd_launch, SHIFT);                     \
+        return fwd_launch<TS, TB, SHIFT, k, 768>(a, s, st);     \
+    }
+#define GDN2_BWD(SHIFT)                                         \
+    {                                                           \
+        GDN2_UP_TO(64, bwd_launch, SHIFT);                      \
+        GDN2_UP_TO(128, bwd_launch, SHIFT);                     \
+        GDN2_UP_TO(192, bwd_launch, SHIFT);                     \
+        GDN2_UP_TO(256, bwd_launch, SHIFT);                     \
+        GDN2_UP_TO(320, bwd_launch, SHIFT);                     \
+        GDN2_UP_TO(512, bwd_launch, SHIFT);                     \
+        GDN2_UP_TO(640, bwd_launch, SHIFT);                     \
+        return bwd_launch<TS, TB, SHIFT, k, 768>(a, s, st);     \
     }
 
 template <typename TS, typename TB> cudaError_t fwd_sized(const FwdArgs &a, cudaStream_t st) {
@@ -728,8 +743,8 @@ template <typename TS, typename TB> cudaError_t fwd_sized(const FwdArgs &a, cuda
     if (s.more) return fwd_launch<TS, TB, true, k + 1, 1024>(a, s, st);
     if (s.threads > 768)
         return s.shift ? fwd_launch<TS, TB, true, k, 1024>(a, s, st) : fwd_launch<TS, TB, false, k, 1024>(a, s, st);
-    if (s.shift) GDN2_BY_THREADS(fwd_launch, true)
-    GDN2_BY_THREADS(fwd_launch, false)
+    if (s.shift) GDN2_FWD(true)
+    GDN2_FWD(false)
 }
 template <typename TS, typename TB> cudaError_t bwd_sized(const BwdArgs &a, cudaStream_t st) {
     constexpr int V = vector_channels<TS, TB>(), k = 8 / V;
@@ -738,10 +753,12 @@ template <typename TS, typename TB> cudaError_t bwd_sized(const BwdArgs &a, cuda
         if (s.threads > 512) return bwd_launch<TS, TB, true, 2 * k, 544>(a, s, st);
         return s.shift ? bwd_launch<TS, TB, true, 2 * k, 512>(a, s, st) : bwd_launch<TS, TB, false, 2 * k, 512>(a, s, st);
     }
-    if (s.shift) GDN2_BY_THREADS(bwd_launch, true)
-    GDN2_BY_THREADS(bwd_launch, false)
+    if (s.shift) GDN2_BWD(true)
+    GDN2_BWD(false)
 }
-#undef GDN2_BY_THREADS
+#undef GDN2_FWD
+#undef GDN2_BWD
+#undef GDN2_UP_TO
 
 // CTAs of the backward: the workspace holds one row of partial sums for each, so
 // the count goes by the sizes alone (148 SMs).
