@@ -407,7 +407,7 @@ residual_norm_kernel(const TS *x, const TB *r, const float *__restrict__ weight,
 // row of `part` ([gridDim][1 or 2][D]); reduce_parts_kernel adds those in a fixed
 // order, so the result does not change from call to call.
 // CTAs of the backward on an SM: 512 threads of 128 registers, or, where that would leave much
-// of the SM idle, three CTAs of 192 (112 registers) or two of 320 (96): 13,107 x 2,560 BF16 74
+// of the SM idle, three CTAs of 192 or two of 320 (96 registers each): 13,107 x 2,560 BF16 74
 // us, 96 with one CTA.  One CTA of more than 512 threads has 96 registers at 640, 80 at 768.
 constexpr int bwd_ctas(int maxt) { return maxt == 192 ? 3 : maxt == 320 ? 2 : maxt <= 512 ? 512 / maxt : 1; }
 // Those with fewer than 128 registers, and 16 channels a thread, keep weight and scale in shared memory.
