@@ -23,11 +23,12 @@
 // channels stay the same from row to row, and only the vectors at a row's two ends are
 // masked when read and written element by element.
 //
-// Measured on a B200, 16,384 x 2,048, residual scale and p = 0.1: forward, BF16,
-// 49.8 us = 5.39 TB/s (45 us without dropout); FP32 stream and BF16 branch 66 us = 6.10
-// TB/s; backward, FP32 stream, 95.6 us = 6.32 TB/s (98 % of a copy's rate), BF16 74 us =
-// 5.45 TB/s, bound there by the mask's and the conversions' instructions.  6,553 x 5,120: 53,
-// 63, 100 and 78 us; 4,096 x 8,192: 53, 68, 116 and 99 us.  Shifted rows: 32,768 x 1,001
+// Measured on a B200, 16,384 x 2,048, residual scale and p = 0.1 (1 to 3 % between sessions):
+// forward, BF16, 50 us = 5.37 TB/s (45 us without dropout); FP32 stream and BF16 branch 67 us =
+// 6.0 TB/s, both FP32 94; backward, FP32 stream, 95.9 us = 6.30 TB/s (97 % of a copy's rate),
+// BF16 75 us = 5.4 TB/s, bound there by the mask's and the conversions' instructions, both FP32
+// 120.  Forward with a BF16 and an FP32 stream, backward with an FP32 and a BF16 one: 6,553 x
+// 5,120 55, 63, 100 and 80 us; 4,096 x 8,192 53, 68, 116 and 99 us.  Shifted rows: 32,768 x 1,001
 // forward without dropout 49.5 us = 5.30 TB/s; 16,384 x 2,047 with it, BF16, 87 us and
 // backward 125 us, bound by putting the mask together and by the rows' ends.
 #include "async_copy.cuh"
